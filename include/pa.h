@@ -38,8 +38,9 @@
  *   - Kernels launch as programmatic dependents of the work before them in
  *     the stream and wait for it on the device before touching its data,
  *     with one exception: the decode kernels read seq_lens to split the work
- *     before that wait.  No kernel of this library writes seq_lens; a kernel
- *     of the caller's that produces seq_lens and lets dependents start early
+ *     before that wait.  The kernels of this library that write seq_lens
+ *     (pa_append_slots_device, pa_trim_slots_device) do not let dependents
+ *     start early; a kernel of the caller's that produces seq_lens and does
  *     (griddepcontrol.launch_dependents) must not directly precede a decode
  *     call.  Ordinary stream order (copies, kernels without that trigger)
  *     needs nothing.
@@ -88,6 +89,8 @@ typedef enum pa_kv_dtype {
 #define PA_DEVERR_BAD_PAIR     0x8u /* copy pair id/length outside the pool */
 #define PA_DEVERR_TIMEOUT      0x10u /* a pipeline wait hit its bound       */
 #define PA_DEVERR_LAUNCH       0x20u /* internal launch-layout check failed */
+#define PA_DEVERR_OUT_OF_BLOCKS 0x40u /* device free list exhausted         */
+#define PA_DEVERR_BAD_QUERY    0x80u /* query offsets out of order or range */
 
 /* Version of this ABI; bumped on any incompatible change. */
 int32_t pa_abi_version(void);
@@ -481,6 +484,129 @@ pa_status pa_decode_noalloc(const void* q, const void* k_cache,
                             int32_t head_dim, int32_t block_size,
                             int32_t num_blocks, float scale, void* out,
                             int32_t num_splits, void* stream);
+
+/* ---------------------------------------------------------- prompt side
+ * What a batch needs before and between its decode steps: blocks and slots
+ * for its new tokens without a host round trip, attention of many query
+ * tokens per sequence over the paged cache, and attention to an encoder's
+ * states held in a paged cache.
+ *
+ * Ragged batches: the query tokens of all sequences lie one after another,
+ * sequence b's at rows [q_start[b], q_start[b + 1]).  num_tokens may exceed
+ * q_start[num_seqs] (a batch padded to a fixed size): those rows are left
+ * as they were. */
+
+/* pa_append_slots_device -- block tables and slot maps on the GPU from
+ * request lengths; pa_batch_append_slots with the free list, the tables and
+ * the lengths in device memory.  "Paged Attention and KV Cache
+ * Fragmentation", section "How PagedAttention maps an OS concept onto GPU
+ * memory": blocks are allocated only as a sequence actually grows.  For
+ * b = 0, 1, ... in order, sequence b grows from lens[b] to lens[b] + n_new[b]
+ * tokens: for every block boundary crossed the top id of the stack
+ * free_ids[0 .. *num_free) is popped into the next entry of row b of the
+ * table, and token p of the new ones gets the slot
+ * table[b][p / block_size] * block_size + p % block_size.  Outputs:
+ *   block_tables  new entries only; the others are left as they were
+ *   slot_mapping  int64 [num_tokens], sequence after sequence; rows past the
+ *                 last sequence get -1 (pa_cache_write skips those)
+ *   q_start       int32 [num_seqs + 1], exclusive sums of n_new
+ *   seq_lens      int32 [num_seqs], the new lengths (may be lens itself)
+ *   num_free_out  int32 [1], the stack's new height (may be num_free itself);
+ *                 free_ids is not changed
+ *   num_done      int32 [1], sequences that grew
+ * The first sequence that cannot grow stops the batch, as in the host call:
+ * too few free blocks (PA_DEVERR_OUT_OF_BLOCKS), a negative length or one
+ * past the table (PA_DEVERR_BAD_SEQ_LEN), more tokens than num_tokens
+ * (PA_DEVERR_BAD_QUERY).  It and the sequences behind it keep their lengths
+ * and tables, and their slots are -1.  An id outside the pool, popped or in
+ * the table, gives the slot -1 and flags PA_DEVERR_BAD_BLOCK_ID.
+ * Requirements: a partly filled last block must be private to its sequence
+ * (copy-on-write done); blocks of prompts shared through the host manager
+ * are not on this free list.  Other outputs must not overlap inputs. */
+pa_status pa_append_slots_device(const int32_t* lens, const int32_t* n_new,
+                                 int32_t* block_tables, int32_t max_blocks_per_seq,
+                                 const int32_t* free_ids, const int32_t* num_free,
+                                 int32_t num_seqs, int32_t num_tokens,
+                                 int32_t block_size, int32_t num_blocks,
+                                 int64_t* slot_mapping, int32_t* q_start,
+                                 int32_t* seq_lens, int32_t* num_free_out,
+                                 int32_t* num_done, void* stream);
+
+/* pa_trim_slots_device -- the reverse: sequence b shrinks from lens[b] to
+ * new_lens[b] tokens (0: it has finished; a few less: rejected drafts are
+ * taken back).  Its blocks from ceil(new_lens[b] / block_size) on are pushed
+ * onto free_ids (capacity num_blocks), sequence after sequence, each in
+ * table order.  seq_lens (may be lens itself) gets the new lengths,
+ * num_free_out (may be num_free itself) the stack's new height; the tables
+ * are only read.  A sequence whose new length is negative or past its old
+ * one flags PA_DEVERR_BAD_SEQ_LEN; one that would release an id outside the
+ * pool, or more blocks than the stack has room for, flags
+ * PA_DEVERR_BAD_BLOCK_ID; such sequences keep their length and blocks.
+ * The released blocks must be private to their sequence. */
+pa_status pa_trim_slots_device(const int32_t* lens, const int32_t* new_lens,
+                               const int32_t* block_tables, int32_t max_blocks_per_seq,
+                               int32_t* free_ids, const int32_t* num_free,
+                               int32_t num_seqs, int32_t block_size, int32_t num_blocks,
+                               int32_t* seq_lens, int32_t* num_free_out, void* stream);
+
+/* pa_attention_workspace_size -- bytes of device workspace pa_prefill and
+ * pa_cross_attention need for this shape with `num_splits` work partitions
+ * (0 = one per SM).  Independent of the numbers of tokens. */
+pa_status pa_attention_workspace_size(int32_t num_seqs, int32_t num_q_heads,
+                                      int32_t num_kv_heads, int32_t head_dim,
+                                      int32_t num_splits, size_t* bytes);
+
+/* pa_prefill -- causal attention of each sequence's newest tokens over its
+ * paged cache: a whole prompt, a chunk of one, or a few drafted tokens.  The
+ * tokens' K and V are in the cache already (pa_cache_write).  For sequence
+ * b with nq = q_start[b + 1] - q_start[b] query tokens and n = seq_lens[b]
+ * cached ones (the queries' own included), query i is the token at position
+ * n - nq + i and sees positions 0 .. n - nq + i; with g = h / (num_q_heads /
+ * num_kv_heads) and K_b, V_b as in pa_decode:
+ *     out[q_start[b] + i][h] = sum_t softmax(scale <q, K_b[t]>)_t V_b[t]
+ * with fp32 products and sums; the softmax weights meet V as bf16.  FP8
+ * caches with q_start are not implemented (PA_ERR_UNSUPPORTED).
+ *   q, out       device bf16 [num_tokens][num_q_heads][head_dim]
+ *   q_start      device int32 [num_seqs + 1], ascending, within
+ *                [0, num_tokens]; NULL: one token per sequence
+ *   seq_lens     device int32 [num_seqs]
+ *   workspace    >= pa_attention_workspace_size() bytes, 16-byte aligned (no
+ *                initialisation needed; one call at a time may use it)
+ * other arguments as pa_decode.  Supported: head_dim in {64, 128};
+ * 1 <= num_q_heads / num_kv_heads <= 64; block_size a power of two in
+ * [8, 256].  Offsets out of order or range flag PA_DEVERR_BAD_QUERY and
+ * nothing is written.  Lengths outside the table are clamped and flag
+ * PA_DEVERR_BAD_SEQ_LEN; so do more queries than tokens (nq > n), which
+ * yield zeros.  Table entries outside the pool read as zeros and flag
+ * PA_DEVERR_BAD_BLOCK_ID.  Cache slots past a sequence's end are never
+ * used, whatever they hold; a NaN or infinity in V at a position that some
+ * query of the same call does see may reach other queries of the sequence. */
+pa_status pa_prefill(const void* q, const void* k_cache, const void* v_cache,
+                     const float* k_scale, const float* v_scale, pa_kv_dtype kv_dtype,
+                     const int32_t* block_tables, int32_t max_blocks_per_seq,
+                     const int32_t* q_start, const int32_t* seq_lens, int32_t num_seqs,
+                     int32_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads,
+                     int32_t head_dim, int32_t block_size, int32_t num_blocks,
+                     float scale, void* out, void* workspace, size_t workspace_bytes,
+                     int32_t num_splits, void* stream);
+
+/* pa_cross_attention -- attention of a decoder's tokens to an encoder's
+ * states of another length, held in a paged cache of their own: pa_prefill
+ * without the causal limit.  Every query token of sequence b sees all
+ * seq_lens[b] encoder states; none (0) gives zeros.  Sequences may share
+ * encoder blocks through their tables.  q_start == NULL is the decode step,
+ * one token per sequence (num_tokens == num_seqs); with at most 8 query
+ * heads per KV head that step runs pa_decode's kernels, and seq_lens is then
+ * read early, as there. */
+pa_status pa_cross_attention(const void* q, const void* k_cache, const void* v_cache,
+                             const float* k_scale, const float* v_scale,
+                             pa_kv_dtype kv_dtype, const int32_t* block_tables,
+                             int32_t max_blocks_per_seq, const int32_t* q_start,
+                             const int32_t* seq_lens, int32_t num_seqs, int32_t num_tokens,
+                             int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                             int32_t block_size, int32_t num_blocks, float scale, void* out,
+                             void* workspace, size_t workspace_bytes, int32_t num_splits,
+                             void* stream);
 
 /* ------------------------------------------------------- block manager
  * Host-only block allocator ("Paged Attention and KV Cache Fragmentation",

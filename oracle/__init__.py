@@ -14,6 +14,9 @@ paged_attention
     Cache write (scatter append), block copy (copy-on-write) and paged decode
     attention: gather each sequence's K/V through its block table into a
     contiguous fp64 array, then dense softmax(q K^T * scale) V.
+prompt
+    Ragged attention over a paged cache: causal (prompts, chunks, drafted
+    tokens) and cross (a decoder's tokens over an encoder's states).
 e4m3
     OCP OFP8 E4M3 codec written from the format definition (decode table and a
     round-to-nearest-even, saturating fp32 -> E4M3 encoder).

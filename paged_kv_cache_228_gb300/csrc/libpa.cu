@@ -1,8 +1,7 @@
 // libpa: C ABI entry points (declared in include/pa.h).  Host-side argument
 // validation, TMA descriptor encoding and kernel launches; the kernels live
-// in decode.cuh, nvfp4.cuh, cascade.cuh and cache_ops.cuh, the host block
-// manager in
-// block_manager.cpp.
+// in decode.cuh, nvfp4.cuh, cascade.cuh, prefill.cuh, slots.cuh and
+// cache_ops.cuh, the host block manager in block_manager.cpp.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
@@ -22,6 +21,8 @@
 #include "nvfp4.cuh"
 #include "pa.h"
 #include "pa_testing.h"
+#include "prefill.cuh"
+#include "slots.cuh"
 
 namespace pa {
 
@@ -1295,4 +1296,311 @@ extern "C" pa_status pa_decode_append_nvfp4(
                           max_blocks_per_seq, seq_lens, num_seqs, num_q_heads, num_kv_heads,
                           head_dim, block_size, num_blocks, scale, out, workspace,
                           workspace_bytes, num_splits, stream, &app);
+}
+
+// ------------------------------------------------------------ prompt side
+namespace pa {
+namespace {
+
+// The slot kernels: a cluster of kC CTAs, a programmatic dependent of the
+// work before it.
+template <int kC>
+pa_status launch_slots(void (*kernel)(SlotParams), const SlotParams& p, cudaStream_t stream) {
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kC;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kC);
+  cfg.blockDim = dim3(kSlThreads);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = kC == 1 ? 1 : 2;
+  return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+// Tokens (append) or table entries (trim) from which a cluster shares them.
+constexpr int64_t kSlClusterFrom = 4096;
+
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// 4D map of a bf16 pool for the prompt-side kernel: 8-token groups of D / 64
+// slabs of 8 rows x 64 columns; box = one block (at most a chunk) of a head.
+bool encode_pool_4d(CUtensorMap* m, const void* base, int32_t D, int64_t groups,
+                    int32_t box_groups) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t row = static_cast<cuuint64_t>(D) * 2;
+  cuuint64_t dims[4] = {64, 8, static_cast<cuuint64_t>(D / 64), static_cast<cuuint64_t>(groups)};
+  cuuint64_t strides[3] = {row, 128, 8 * row};
+  cuuint32_t box[4] = {64, 8, static_cast<cuuint32_t>(D / 64), static_cast<cuuint32_t>(box_groups)};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+size_t prefill_workspace(int64_t P, int32_t head_dim) {
+  return static_cast<size_t>(2 * P) * kPaItemRows *
+             (static_cast<size_t>(head_dim) * sizeof(float) + sizeof(float2)) +
+         static_cast<size_t>(P) * sizeof(int4);
+}
+
+template <int D>
+pa_status launch_prefill(const PrefillParams& prm_in, const void* k_cache, const void* v_cache,
+                         void* workspace, size_t workspace_bytes, int32_t num_splits,
+                         cudaStream_t stream) {
+  int sms = 0, dev = 0;
+  const pa_status st = device_sms(&sms, &dev);
+  if (st != PA_OK) return st;
+  const int32_t P = num_splits > 0 ? num_splits : sms;
+  const size_t need = prefill_workspace(P, D);
+  if (workspace == nullptr || workspace_bytes < need || !aligned16(workspace))
+    return PA_ERR_WORKSPACE;
+  {
+    static bool attr_set[kMaxDevices] = {false};
+    std::lock_guard<std::mutex> lk(g_mu);
+    if (!attr_set[dev]) {
+      if (cudaFuncSetAttribute(prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               PaSmem<D>::kBytes) != cudaSuccess)
+        return PA_ERR_CUDA;
+      attr_set[dev] = true;
+    }
+  }
+  PrefillParams p = prm_in;
+  p.num_ctas = P;
+  char* w = static_cast<char*>(workspace);
+  p.ws_o = reinterpret_cast<float*>(w);
+  w += static_cast<size_t>(2) * P * kPaItemRows * D * sizeof(float);
+  p.ws_ml = reinterpret_cast<float2*>(w);
+  w += static_cast<size_t>(2) * P * kPaItemRows * sizeof(float2);
+  p.ws_job = reinterpret_cast<int4*>(w);
+  const int32_t box = (p.block_size < kPaChunk ? p.block_size : kPaChunk) / 8;
+  CUtensorMap tk, tv;
+  if (!encode_pool_4d(&tk, k_cache, D, p.groups_total, box) ||
+      !encode_pool_4d(&tv, v_cache, D, p.groups_total, box))
+    return PA_ERR_CUDA;
+  if (launch_pdl(prefill_kernel<D>, dim3(static_cast<unsigned>(P)), dim3(kPaThreads),
+                 PaSmem<D>::kBytes, stream, tk, tv, p) != cudaSuccess)
+    return PA_ERR_CUDA;
+  return launch_pdl(prefill_merge_kernel<D>, dim3(static_cast<unsigned>(P), kPaItemRows / 32),
+                    dim3(256), 0, stream, p) == cudaSuccess
+             ? PA_OK
+             : PA_ERR_CUDA;
+}
+
+constexpr int32_t kPaMaxGroup = 64;
+
+pa_status attention_entry(bool causal, const void* q, const void* k_cache, const void* v_cache,
+                          const float* k_scale, const float* v_scale, pa_kv_dtype kv_dtype,
+                          const int32_t* block_tables, int32_t max_blocks_per_seq,
+                          const int32_t* q_start, const int32_t* seq_lens, int32_t num_seqs,
+                          int32_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads,
+                          int32_t head_dim, int32_t block_size, int32_t num_blocks, float scale,
+                          void* out, void* workspace, size_t workspace_bytes, int32_t num_splits,
+                          void* stream) {
+  const float sl = (scale < 0.f ? -scale : scale) * 1.4426950408889634f;
+  if (num_seqs < 0 || num_tokens < 0 || num_q_heads <= 0 || num_kv_heads <= 0 ||
+      num_blocks <= 0 || max_blocks_per_seq < 0 || num_splits < 0 || num_splits > 65535 ||
+      !(sl <= 3.4028234e38f) || num_q_heads % num_kv_heads != 0)
+    return PA_ERR_INVALID_ARG;
+  if (kv_dtype != PA_KV_BF16 && kv_dtype != PA_KV_FP8_E4M3) return PA_ERR_INVALID_ARG;
+  if (q_start == nullptr && num_tokens != num_seqs) return PA_ERR_INVALID_ARG;
+  const int32_t group = num_q_heads / num_kv_heads;
+  if (head_dim != 64 && head_dim != 128) return PA_ERR_UNSUPPORTED;
+  if (group > kPaMaxGroup) return PA_ERR_UNSUPPORTED;
+  if (!pow2_in(block_size, 8, 256)) return PA_ERR_UNSUPPORTED;
+  if (num_seqs == 0 || num_tokens == 0) return PA_OK;
+  if (!q || !k_cache || !v_cache || !block_tables || !seq_lens || !out) return PA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) ||
+      !aligned4(block_tables) || !aligned4(seq_lens) || !aligned4(q_start) ||
+      !aligned4(k_scale) || !aligned4(v_scale))
+    return PA_ERR_INVALID_ARG;
+  if (kv_dtype == PA_KV_FP8_E4M3 && (!k_scale || !v_scale)) return PA_ERR_INVALID_ARG;
+  const int64_t groups = static_cast<int64_t>(num_blocks) * num_kv_heads * (block_size / 8);
+  if (groups > INT_MAX - 64) return PA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(num_tokens) > INT_MAX - 1024) return PA_ERR_UNSUPPORTED;
+  // a limit plus a chunk and an item stays within 32 bits
+  if (static_cast<int64_t>(max_blocks_per_seq) * block_size > INT_MAX - 1024)
+    return PA_ERR_UNSUPPORTED;
+  if (q_start == nullptr && group <= kMaxG)
+    return decode_entry(q, k_cache, v_cache, k_scale, v_scale, kv_dtype, block_tables,
+                        max_blocks_per_seq, seq_lens, num_seqs, num_q_heads, num_kv_heads,
+                        head_dim, block_size, num_blocks, scale, out, workspace, workspace_bytes,
+                        num_splits, stream, nullptr);
+  if (kv_dtype != PA_KV_BF16) return PA_ERR_UNSUPPORTED;
+
+  PrefillParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.q = static_cast<const uint8_t*>(q);
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.q_start = q_start;
+  p.seq_lens = seq_lens;
+  p.block_tables = block_tables;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.num_seqs = num_seqs;
+  p.num_tokens = num_tokens;
+  p.num_q_heads = num_q_heads;
+  p.num_kv_heads = num_kv_heads;
+  p.group = group;
+  p.tok_per_item = kPaItemRows / group;
+  p.block_size = block_size;
+  p.log2_bs = ilog2(block_size);
+  p.max_blocks = max_blocks_per_seq;
+  p.num_blocks = num_blocks;
+  p.groups_total = static_cast<int32_t>(groups);
+  p.causal = causal ? 1 : 0;
+  // A negative scale acts as its magnitude on the negated query (exact), a
+  // zero one as any scale on a zero query: the kernel's scale is positive.
+  p.q_and = sl > 0.f ? 0xffffffffu : 0u;
+  p.q_xor = scale < 0.f && sl > 0.f ? 0x80008000u : 0u;
+  p.sl = sl > 0.f ? sl : 1.f;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return head_dim == 128
+             ? launch_prefill<128>(p, k_cache, v_cache, workspace, workspace_bytes, num_splits, s)
+             : launch_prefill<64>(p, k_cache, v_cache, workspace, workspace_bytes, num_splits, s);
+}
+
+}  // namespace
+}  // namespace pa
+
+extern "C" pa_status pa_append_slots_device(const int32_t* lens, const int32_t* n_new,
+                                            int32_t* block_tables, int32_t max_blocks_per_seq,
+                                            const int32_t* free_ids, const int32_t* num_free,
+                                            int32_t num_seqs, int32_t num_tokens,
+                                            int32_t block_size, int32_t num_blocks,
+                                            int64_t* slot_mapping, int32_t* q_start,
+                                            int32_t* seq_lens, int32_t* num_free_out,
+                                            int32_t* num_done, void* stream) {
+  const NvtxRange nvtx_range("pa_append_slots_device");
+  if (num_seqs < 0 || num_tokens < 0 || block_size <= 0 || num_blocks <= 0 ||
+      max_blocks_per_seq < 0)
+    return PA_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(max_blocks_per_seq) * block_size > INT_MAX - 1024 ||
+      num_tokens > INT_MAX - 1024)
+    return PA_ERR_UNSUPPORTED;
+  if (!num_free || !q_start || !num_free_out || !num_done || !free_ids) return PA_ERR_INVALID_ARG;
+  if (num_seqs > 0 && (!lens || !n_new || !block_tables || !seq_lens)) return PA_ERR_INVALID_ARG;
+  if (num_tokens > 0 && !slot_mapping) return PA_ERR_INVALID_ARG;
+  if (!aligned4(lens) || !aligned4(n_new) || !aligned4(block_tables) || !aligned4(free_ids) ||
+      !aligned4(num_free) || !aligned4(q_start) || !aligned4(seq_lens) ||
+      !aligned4(num_free_out) || !aligned4(num_done) ||
+      (reinterpret_cast<uintptr_t>(slot_mapping) & 7u))
+    return PA_ERR_INVALID_ARG;
+  SlotParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.lens = lens;
+  p.change = n_new;
+  p.tables = block_tables;
+  p.free_ids = const_cast<int32_t*>(free_ids);
+  p.num_free = num_free;
+  p.slots = slot_mapping;
+  p.q_start = q_start;
+  p.seq_lens = seq_lens;
+  p.num_free_out = num_free_out;
+  p.num_done = num_done;
+  p.num_seqs = num_seqs;
+  p.num_tokens = num_tokens;
+  p.max_blocks = max_blocks_per_seq;
+  p.block_size = block_size;
+  p.num_blocks = num_blocks;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return num_tokens >= kSlClusterFrom
+             ? launch_slots<kSlCluster>(append_slots_kernel<kSlCluster>, p, s)
+             : launch_slots<1>(append_slots_kernel<1>, p, s);
+}
+
+extern "C" pa_status pa_trim_slots_device(const int32_t* lens, const int32_t* new_lens,
+                                          const int32_t* block_tables,
+                                          int32_t max_blocks_per_seq, int32_t* free_ids,
+                                          const int32_t* num_free, int32_t num_seqs,
+                                          int32_t block_size, int32_t num_blocks,
+                                          int32_t* seq_lens, int32_t* num_free_out,
+                                          void* stream) {
+  const NvtxRange nvtx_range("pa_trim_slots_device");
+  if (num_seqs < 0 || block_size <= 0 || num_blocks <= 0 || max_blocks_per_seq < 0)
+    return PA_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(max_blocks_per_seq) * block_size > INT_MAX - 1024)
+    return PA_ERR_UNSUPPORTED;
+  if (!num_free || !num_free_out || !free_ids) return PA_ERR_INVALID_ARG;
+  if (num_seqs > 0 && (!lens || !new_lens || !block_tables || !seq_lens)) return PA_ERR_INVALID_ARG;
+  if (!aligned4(lens) || !aligned4(new_lens) || !aligned4(block_tables) || !aligned4(free_ids) ||
+      !aligned4(num_free) || !aligned4(seq_lens) || !aligned4(num_free_out))
+    return PA_ERR_INVALID_ARG;
+  SlotParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.lens = lens;
+  p.change = new_lens;
+  p.tables = const_cast<int32_t*>(block_tables);
+  p.free_ids = free_ids;
+  p.num_free = num_free;
+  p.seq_lens = seq_lens;
+  p.num_free_out = num_free_out;
+  p.num_seqs = num_seqs;
+  p.max_blocks = max_blocks_per_seq;
+  p.block_size = block_size;
+  p.num_blocks = num_blocks;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return static_cast<int64_t>(num_seqs) * max_blocks_per_seq >= kSlClusterFrom
+             ? launch_slots<kSlCluster>(trim_slots_kernel<kSlCluster>, p, s)
+             : launch_slots<1>(trim_slots_kernel<1>, p, s);
+}
+
+extern "C" pa_status pa_attention_workspace_size(int32_t num_seqs, int32_t num_q_heads,
+                                                 int32_t num_kv_heads, int32_t head_dim,
+                                                 int32_t num_splits, size_t* bytes) {
+  if (bytes == nullptr || num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 ||
+      num_splits < 0 || num_splits > 65535 || num_q_heads % num_kv_heads != 0)
+    return PA_ERR_INVALID_ARG;
+  if (head_dim != 64 && head_dim != 128) return PA_ERR_UNSUPPORTED;
+  if (num_q_heads / num_kv_heads > kPaMaxGroup) return PA_ERR_UNSUPPORTED;
+  int sms = 0;
+  pa_status st = device_sms(&sms, nullptr);
+  if (st != PA_OK) return st;
+  size_t need = prefill_workspace(num_splits > 0 ? num_splits : sms, head_dim);
+  if (num_q_heads / num_kv_heads <= kMaxG) {  // one token a sequence: the decode kernels
+    size_t dec = 0;
+    st = pa_decode_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, num_splits, &dec);
+    if (st != PA_OK) return st;
+    if (dec > need) need = dec;
+  }
+  *bytes = need;
+  return PA_OK;
+}
+
+extern "C" pa_status pa_prefill(const void* q, const void* k_cache, const void* v_cache,
+                                const float* k_scale, const float* v_scale, pa_kv_dtype kv_dtype,
+                                const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                const int32_t* q_start, const int32_t* seq_lens, int32_t num_seqs,
+                                int32_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads,
+                                int32_t head_dim, int32_t block_size, int32_t num_blocks,
+                                float scale, void* out, void* workspace, size_t workspace_bytes,
+                                int32_t num_splits, void* stream) {
+  const NvtxRange nvtx_range("pa_prefill");
+  return attention_entry(true, q, k_cache, v_cache, k_scale, v_scale, kv_dtype, block_tables,
+                         max_blocks_per_seq, q_start, seq_lens, num_seqs, num_tokens, num_q_heads,
+                         num_kv_heads, head_dim, block_size, num_blocks, scale, out, workspace,
+                         workspace_bytes, num_splits, stream);
+}
+
+extern "C" pa_status pa_cross_attention(const void* q, const void* k_cache, const void* v_cache,
+                                        const float* k_scale, const float* v_scale,
+                                        pa_kv_dtype kv_dtype, const int32_t* block_tables,
+                                        int32_t max_blocks_per_seq, const int32_t* q_start,
+                                        const int32_t* seq_lens, int32_t num_seqs,
+                                        int32_t num_tokens, int32_t num_q_heads,
+                                        int32_t num_kv_heads, int32_t head_dim,
+                                        int32_t block_size, int32_t num_blocks, float scale,
+                                        void* out, void* workspace, size_t workspace_bytes,
+                                        int32_t num_splits, void* stream) {
+  const NvtxRange nvtx_range("pa_cross_attention");
+  return attention_entry(false, q, k_cache, v_cache, k_scale, v_scale, kv_dtype, block_tables,
+                         max_blocks_per_seq, q_start, seq_lens, num_seqs, num_tokens, num_q_heads,
+                         num_kv_heads, head_dim, block_size, num_blocks, scale, out, workspace,
+                         workspace_bytes, num_splits, stream);
 }

@@ -9,8 +9,9 @@ falling back to anything else.
 Ordering of ``seq_lens``: every decode call (pa_decode*, pa_decode_cascade,
 pa_decode_noalloc) launches as a programmatic dependent of the work before
 it on the stream and reads ``seq_lens`` to split its work BEFORE it waits
-for that work.  Nothing in this library writes ``seq_lens``.  If a kernel of
-yours writes ``seq_lens`` and calls ``griddepcontrol.launch_dependents``
+for that work.  The calls of this library that write ``seq_lens``
+(pa_append_slots_device, pa_trim_slots_device) do not let their dependents
+start early, so a decode call may follow them.  If a kernel of yours writes ``seq_lens`` and calls ``griddepcontrol.launch_dependents``
 (lets its dependents start early), do not launch a decode call directly
 after it on the same stream: put a copy or any kernel
 without that trigger in between.  Ordinary stream order (torch ops, copies)
@@ -34,6 +35,7 @@ PA_KV_BF16, PA_KV_FP8_E4M3, PA_KV_NVFP4 = 0, 1, 2
 
 DEVERR_BAD_BLOCK_ID, DEVERR_BAD_SEQ_LEN, DEVERR_BAD_SLOT = 0x1, 0x2, 0x4
 DEVERR_BAD_PAIR, DEVERR_TIMEOUT, DEVERR_LAUNCH = 0x8, 0x10, 0x20
+DEVERR_OUT_OF_BLOCKS, DEVERR_BAD_QUERY = 0x40, 0x80
 
 _lib = None
 
@@ -92,6 +94,20 @@ SIGNATURES = {
                                         _c_ptr, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int,
                                         ctypes.c_float, _c_ptr, _c_ptr, _c_size, _c_int,
                                         _c_ptr]),
+    "pa_append_slots_device": (_c_int, [_c_ptr, _c_ptr, _c_ptr, _c_int, _c_ptr, _c_ptr, _c_int,
+                                        _c_int, _c_int, _c_int, _c_ptr, _c_ptr, _c_ptr, _c_ptr,
+                                        _c_ptr, _c_ptr]),
+    "pa_trim_slots_device": (_c_int, [_c_ptr, _c_ptr, _c_ptr, _c_int, _c_ptr, _c_ptr, _c_int,
+                                      _c_int, _c_int, _c_ptr, _c_ptr, _c_ptr]),
+    "pa_attention_workspace_size": (_c_int, [_c_int, _c_int, _c_int, _c_int, _c_int,
+                                             ctypes.POINTER(_c_size)]),
+    "pa_prefill": (_c_int, [_c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_int, _c_ptr, _c_int,
+                            _c_ptr, _c_ptr, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int,
+                            _c_int, ctypes.c_float, _c_ptr, _c_ptr, _c_size, _c_int, _c_ptr]),
+    "pa_cross_attention": (_c_int, [_c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_int, _c_ptr,
+                                    _c_int, _c_ptr, _c_ptr, _c_int, _c_int, _c_int, _c_int,
+                                    _c_int, _c_int, _c_int, ctypes.c_float, _c_ptr, _c_ptr,
+                                    _c_size, _c_int, _c_ptr]),
     "pa_allocator_create": (_c_int, [_c_int, ctypes.POINTER(_c_ptr)]),
     "pa_allocator_destroy": (None, [_c_ptr]),
     "pa_block_alloc": (_c_int, [_c_ptr, _c_int, _c_ptr]),
@@ -472,6 +488,156 @@ def pa_decode_noalloc(q, k_cache, v_cache, block_tables, seq_lens, scale, out,
         _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
         _kv_dtype(k_cache), _ptr(block_tables), block_tables.shape[1], _ptr(seq_lens), B,
         hq, hkv, d, bs, nb, float(scale), _ptr(out), num_splits, _stream(stream)))
+
+
+# ----------------------------------------------------------- prompt side ---
+def _same_device(*named):
+    """The one CUDA device of the given (name, tensor or None) pairs.  Unlike
+    the decode calls, the prompt-side calls may be made while another device
+    is current: they run on their tensors' device."""
+    dev = None
+    for name, t in named:
+        if t is None:
+            continue
+        if t.device.type != "cuda":
+            raise ValueError(f"{name}: must be a CUDA tensor, is on {t.device}")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"{name}: is on {t.device}, the others on {dev}")
+    return dev
+
+
+def _stream_of(stream, dev):
+    return _stream(torch.cuda.current_stream(dev) if stream is None else stream)
+
+
+def _shape(t, shape, name):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def pa_append_slots_device(lens, n_new, block_tables, free_ids, num_free, block_size,
+                           slot_mapping, q_start, seq_lens, num_free_out, num_done, stream=None):
+    """Grow sequence b from lens[b] by n_new[b] tokens on the GPU: new table
+    entries from the stack free_ids[0 .. num_free), the new tokens' slots,
+    the query offsets q_start [B + 1] and seq_lens.  seq_lens may be lens,
+    num_free_out may be num_free.  len(slot_mapping) is the token capacity
+    (rows past the last sequence get -1)."""
+    B = lens.shape[0]
+    for t, name, n in ((lens, "lens", B), (n_new, "n_new", B), (free_ids, "free_ids", None),
+                       (num_free, "num_free", 1), (q_start, "q_start", B + 1),
+                       (seq_lens, "seq_lens", B), (num_free_out, "num_free_out", 1),
+                       (num_done, "num_done", 1)):
+        _need(t, torch.int32, name, 1)
+        if n is not None:
+            _shape(t, (n,), name)
+    _need(block_tables, torch.int32, "block_tables", 2)
+    _shape(block_tables, (B, block_tables.shape[1]), "block_tables")
+    _need(slot_mapping, torch.int64, "slot_mapping", 1)
+    dev = _same_device(("lens", lens), ("n_new", n_new), ("block_tables", block_tables),
+                       ("free_ids", free_ids), ("num_free", num_free),
+                       ("slot_mapping", slot_mapping), ("q_start", q_start),
+                       ("seq_lens", seq_lens), ("num_free_out", num_free_out),
+                       ("num_done", num_done))
+    with torch.cuda.device(dev):
+        _check("pa_append_slots_device", lib().pa_append_slots_device(
+            _ptr(lens), _ptr(n_new), _ptr(block_tables), block_tables.shape[1], _ptr(free_ids),
+            _ptr(num_free), B, slot_mapping.shape[0], block_size, free_ids.shape[0],
+            _ptr(slot_mapping), _ptr(q_start), _ptr(seq_lens), _ptr(num_free_out),
+            _ptr(num_done), _stream_of(stream, dev)))
+
+
+def pa_trim_slots_device(lens, new_lens, block_tables, free_ids, num_free, block_size, seq_lens,
+                         num_free_out, stream=None):
+    """Shrink sequence b from lens[b] to new_lens[b] tokens on the GPU: its
+    blocks behind the new length are pushed onto free_ids.  seq_lens may be
+    lens, num_free_out may be num_free."""
+    B = lens.shape[0]
+    for t, name, n in ((lens, "lens", B), (new_lens, "new_lens", B), (free_ids, "free_ids", None),
+                       (num_free, "num_free", 1), (seq_lens, "seq_lens", B),
+                       (num_free_out, "num_free_out", 1)):
+        _need(t, torch.int32, name, 1)
+        if n is not None:
+            _shape(t, (n,), name)
+    _need(block_tables, torch.int32, "block_tables", 2)
+    _shape(block_tables, (B, block_tables.shape[1]), "block_tables")
+    dev = _same_device(("lens", lens), ("new_lens", new_lens), ("block_tables", block_tables),
+                       ("free_ids", free_ids), ("num_free", num_free), ("seq_lens", seq_lens),
+                       ("num_free_out", num_free_out))
+    with torch.cuda.device(dev):
+        _check("pa_trim_slots_device", lib().pa_trim_slots_device(
+            _ptr(lens), _ptr(new_lens), _ptr(block_tables), block_tables.shape[1],
+            _ptr(free_ids), _ptr(num_free), B, block_size, free_ids.shape[0], _ptr(seq_lens),
+            _ptr(num_free_out), _stream_of(stream, dev)))
+
+
+def pa_attention_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim,
+                                num_splits=0) -> int:
+    n = _c_size(0)
+    _check("pa_attention_workspace_size", lib().pa_attention_workspace_size(
+        num_seqs, num_q_heads, num_kv_heads, head_dim, num_splits, ctypes.byref(n)))
+    return int(n.value)
+
+
+def _attention(fn, q, k_cache, v_cache, block_tables, q_start, seq_lens, scale, out, workspace,
+               k_scale, v_scale, num_splits, stream):
+    _need(q, torch.bfloat16, "q", 3)
+    _need(out, torch.bfloat16, "out", 3)
+    _shape(out, q.shape, "out")
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        _need(t, k_cache.dtype, name, 4)
+        _shape(t, k_cache.shape, name)
+    _need(block_tables, torch.int32, "block_tables", 2)
+    _need(seq_lens, torch.int32, "seq_lens", 1)
+    T, hq, d = q.shape
+    nb, hkv, bs, d2 = k_cache.shape
+    B = seq_lens.shape[0]
+    if d2 != d:
+        raise ValueError(f"{fn}: head_dim of q is {d}, of the cache {d2}")
+    _shape(block_tables, (B, block_tables.shape[1]), "block_tables")
+    if q_start is not None:
+        _need(q_start, torch.int32, "q_start", 1)
+        _shape(q_start, (B + 1,), "q_start")
+    kv = _kv_dtype(k_cache)
+    if kv == PA_KV_FP8_E4M3:
+        for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            if t is None:
+                raise ValueError(f"{fn}: an FP8 cache needs {name}")
+            _need(t, torch.float32, name, 2)
+            _shape(t, (nb, hkv), name)
+    elif k_scale is not None or v_scale is not None:
+        raise ValueError(f"{fn}: a bf16 cache takes no scales")
+    dev = _same_device(("q", q), ("k_cache", k_cache), ("v_cache", v_cache),
+                       ("block_tables", block_tables), ("q_start", q_start),
+                       ("seq_lens", seq_lens), ("out", out), ("workspace", workspace),
+                       ("k_scale", k_scale), ("v_scale", v_scale))
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    with torch.cuda.device(dev):
+        _check(fn, getattr(lib(), fn)(
+            _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), kv,
+            _ptr(block_tables), block_tables.shape[1], _ptr(q_start), _ptr(seq_lens), B, T, hq,
+            hkv, d, bs, nb, float(scale), _ptr(out), _ptr(workspace), ws_bytes, num_splits,
+            _stream_of(stream, dev)))
+
+
+def pa_prefill(q, k_cache, v_cache, block_tables, q_start, seq_lens, scale, out, workspace=None,
+               k_scale=None, v_scale=None, num_splits=0, stream=None):
+    """Causal attention of each sequence's newest tokens over its paged
+    cache: q, out [T, Hq, d] (bf16), sequence b's tokens at rows
+    [q_start[b], q_start[b + 1]), the last of them at position
+    seq_lens[b] - 1.  Their K and V are in the cache already."""
+    _attention("pa_prefill", q, k_cache, v_cache, block_tables, q_start, seq_lens, scale, out,
+               workspace, k_scale, v_scale, num_splits, stream)
+
+
+def pa_cross_attention(q, k_cache, v_cache, block_tables, q_start, seq_lens, scale, out,
+                       workspace=None, k_scale=None, v_scale=None, num_splits=0, stream=None):
+    """Attention of a decoder's tokens to an encoder's states in a paged
+    cache: every token of sequence b sees all seq_lens[b] states.  q_start
+    None: one token per sequence."""
+    _attention("pa_cross_attention", q, k_cache, v_cache, block_tables, q_start, seq_lens, scale,
+               out, workspace, k_scale, v_scale, num_splits, stream)
 
 
 # --------------------------------------------------------- block manager ---
