@@ -1344,6 +1344,24 @@ bool encode_pool_4d(CUtensorMap* m, const void* base, int32_t D, int64_t groups,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// 4D map of the query tokens: 64 columns x heads x tokens x slabs; box = one
+// slab of a KV head's group for the tokens of a tile.
+bool encode_queries_4d(CUtensorMap* m, const void* base, int32_t D, int32_t heads, int32_t tokens,
+                       int32_t group, int32_t tile_tokens) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t row = static_cast<cuuint64_t>(D) * 2;
+  cuuint64_t dims[4] = {64, static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(tokens),
+                        static_cast<cuuint64_t>(D / 64)};
+  cuuint64_t strides[3] = {row, row * heads, 128};
+  cuuint32_t box[4] = {64, static_cast<cuuint32_t>(group), static_cast<cuuint32_t>(tile_tokens), 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 size_t prefill_workspace(int64_t P, int32_t head_dim) {
   return static_cast<size_t>(2 * P) * kPaItemRows *
              (static_cast<size_t>(head_dim) * sizeof(float) + sizeof(float2)) +
@@ -1365,6 +1383,10 @@ pa_status launch_prefill(const PrefillParams& prm_in, const void* k_cache, const
     static bool attr_set[kMaxDevices] = {false};
     std::lock_guard<std::mutex> lk(g_mu);
     if (!attr_set[dev]) {
+      // the register split takes the launch's registers for granted
+      cudaFuncAttributes fa;
+      if (cudaFuncGetAttributes(&fa, prefill_kernel<D>) != cudaSuccess) return PA_ERR_CUDA;
+      if (fa.numRegs < kPaRegs) return PA_ERR_UNSUPPORTED;
       if (cudaFuncSetAttribute(prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                PaSmem<D>::kBytes) != cudaSuccess)
         return PA_ERR_CUDA;
@@ -1373,6 +1395,7 @@ pa_status launch_prefill(const PrefillParams& prm_in, const void* k_cache, const
   }
   PrefillParams p = prm_in;
   p.num_ctas = P;
+  p.allow_dual = D == 64;
   char* w = static_cast<char*>(workspace);
   p.ws_o = reinterpret_cast<float*>(w);
   w += static_cast<size_t>(2) * P * kPaItemRows * D * sizeof(float);
@@ -1380,12 +1403,13 @@ pa_status launch_prefill(const PrefillParams& prm_in, const void* k_cache, const
   w += static_cast<size_t>(2) * P * kPaItemRows * sizeof(float2);
   p.ws_job = reinterpret_cast<int4*>(w);
   const int32_t box = (p.block_size < kPaChunk ? p.block_size : kPaChunk) / 8;
-  CUtensorMap tk, tv;
-  if (!encode_pool_4d(&tk, k_cache, D, p.groups_total, box) ||
+  CUtensorMap tk, tv, tq;
+  if (!encode_queries_4d(&tq, p.q, D, p.num_q_heads, p.num_tokens, p.group, p.tok_per_tile) ||
+      !encode_pool_4d(&tk, k_cache, D, p.groups_total, box) ||
       !encode_pool_4d(&tv, v_cache, D, p.groups_total, box))
     return PA_ERR_CUDA;
   if (launch_pdl(prefill_kernel<D>, dim3(static_cast<unsigned>(P)), dim3(kPaThreads),
-                 PaSmem<D>::kBytes, stream, tk, tv, p) != cudaSuccess)
+                 PaSmem<D>::kBytes, stream, tk, tv, tq, p) != cudaSuccess)
     return PA_ERR_CUDA;
   return launch_pdl(prefill_merge_kernel<D>, dim3(static_cast<unsigned>(P), kPaItemRows / 32),
                     dim3(256), 0, stream, p) == cudaSuccess
@@ -1448,13 +1472,15 @@ pa_status attention_entry(bool causal, const void* q, const void* k_cache, const
   p.num_q_heads = num_q_heads;
   p.num_kv_heads = num_kv_heads;
   p.group = group;
-  p.tok_per_item = kPaItemRows / group;
+  p.tok_per_tile = kPaRows / group;
+  p.tok_per_item = kPaTiles * p.tok_per_tile;
   p.block_size = block_size;
   p.log2_bs = ilog2(block_size);
   p.max_blocks = max_blocks_per_seq;
   p.num_blocks = num_blocks;
   p.groups_total = static_cast<int32_t>(groups);
   p.causal = causal ? 1 : 0;
+  p.div_group = group == 1 ? 0u : static_cast<uint32_t>((0x100000000ull + group - 1) / group);
   // A negative scale acts as its magnitude on the negated query (exact), a
   // zero one as any scale on a zero query: the kernel's scale is positive.
   p.q_and = sl > 0.f ? 0xffffffffu : 0u;
