@@ -1395,7 +1395,6 @@ pa_status launch_prefill(const PrefillParams& prm_in, const void* k_cache, const
   }
   PrefillParams p = prm_in;
   p.num_ctas = P;
-  p.allow_dual = D == 64;
   char* w = static_cast<char*>(workspace);
   p.ws_o = reinterpret_cast<float*>(w);
   w += static_cast<size_t>(2) * P * kPaItemRows * D * sizeof(float);

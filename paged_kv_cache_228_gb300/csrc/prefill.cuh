@@ -48,7 +48,6 @@ struct PrefillParams {
   int32_t groups_total;      // 8-row groups of the pool (one past the last: reads zeros)
   int32_t num_ctas;
   int32_t causal;
-  int32_t allow_dual;        // the ring is deep enough for both tiles' own chunks
   uint32_t div_group;        // ceil(2^32 / group) for pa_div; 0 when group is 1
   uint32_t q_and, q_xor;     // applied to the query words: negation, or zero
   float sl;                  // |scale| * log2(e), > 0
@@ -58,9 +57,9 @@ constexpr int kPaRows = 128;           // rows per tile (the MMA's M)
 constexpr int kPaTiles = 2;
 constexpr int kPaItemRows = kPaRows * kPaTiles;
 constexpr int kPaChunk = 128;          // tokens per chunk
-// Warps: 0 copies K and V, 1 issues the MMAs, 2 walks the items and loads
-// their queries, 3 is idle (the register split takes whole warpgroups); 4-7
-// and 8-11 are the softmax of tile 0 and 1.
+// Warps: 0 copies K and V, 1 walks the items and loads their queries, 2 and
+// 3 issue the MMAs of tile 0 and 1; 4-7 and 8-11 are the softmax of tile 0
+// and 1.
 constexpr int kPaWarps = 12;
 constexpr int kPaThreads = 32 * kPaWarps;
 constexpr int kPaSoftWarp = 4;
@@ -83,6 +82,7 @@ template <int D>
 struct PaSmem {
   static constexpr int kKV = kPaChunk * D * 2;  // K (or V) of a chunk
   static constexpr int kStages = D == 64 ? 12 : 5;  // one ring: K_j, V_j, K_j+1, ...
+  static constexpr bool kDual = kStages >= 8;
   static constexpr int kQ = kPaRows * D * 2;    // one query tile
   static constexpr int kOffRing = kPaTiles * kQ;
   static constexpr int kOffMl = kOffRing + kStages * kKV;  // tile 1's (m, l), folded by tile 0
@@ -118,7 +118,8 @@ struct PaBars {
   uint64_t p_full[kPaTiles];  // P of the tile's chunk written
   uint64_t o_last[kPaTiles];  // the tile's last product of the item done
   uint64_t ml_full, o_free;   // dual items: tile 1's (m, l) written; its O read
-  uint64_t mma_done;
+  uint64_t turn[kPaTiles];    // the other tile's MMAs of its turn have been issued
+  uint64_t mma_done[kPaTiles];
   int64_t scan[kPaWarps];
   int64_t first_u;            // the CTA's first sequence: units before it
   int32_t first_b;
@@ -127,6 +128,18 @@ struct PaBars {
 };
 static_assert(sizeof(PaBars) <= kPaBarBytes, "barrier block");
 
+// Bounded wait, as mbar_wait; kept to a short loop (not unrolled), since
+// this kernel has some thirty of them and its roles share the SM's
+// instruction cache.
+__device__ __forceinline__ bool pa_wait(uint32_t bar, uint32_t parity,
+                                        uint32_t limit = (1u << 22)) {
+#pragma unroll 1
+  for (uint32_t i = 0; i < limit; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  flag_error(PA_DEVERR_TIMEOUT);
+  return false;
+}
+
 // x / group for a row x of an item (below 2^16, where the rounded-up
 // reciprocal is exact).
 __device__ __forceinline__ uint32_t pa_div(const PrefillParams& p, uint32_t x) {
@@ -134,10 +147,24 @@ __device__ __forceinline__ uint32_t pa_div(const PrefillParams& p, uint32_t x) {
 }
 
 // ------------------------------------------------------------- the plan ---
-// sum_{i < n} floor((a i + b) / m), all arguments non-negative.
-__device__ __forceinline__ int64_t floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
+// sum_{i < n} floor((a i + b) / 128), with a < 2^16 and a n + b < 2^32.
+__device__ __forceinline__ int64_t floor_sum(uint32_t n, uint32_t a, uint32_t b) {
+  uint32_t m = 128;
+  if ((a & (a - 1)) == 0) {
+    // a = 2^k.  From 128 on: a multiple of the divisor.  Below, with q = 128
+    // / a and x = i + b / a, the terms are floor(x / q): a sum of steps.
+    const int k = 31 - __clz(a);
+    if (k >= 7)
+      return (static_cast<int64_t>(n) * (n - 1) / 2 << (k - 7)) + static_cast<int64_t>(n) * (b >> 7);
+    auto steps = [&](uint32_t x) {  // sum_{y < x} floor(y / q)
+      const int64_t w = x >> (7 - k), r = x - (w << (7 - k));
+      return (w * (w - 1) / 2 << (7 - k)) + w * r;
+    };
+    return steps((b >> k) + n) - steps(b >> k);
+  }
   int64_t s = 0;
-  while (n > 0) {
+#pragma unroll 1
+  while (n > 0) {  // the Euclidean recursion on (m, a)
     if (a >= m) {
       s += static_cast<int64_t>(n) * (n - 1) / 2 * (a / m);
       a %= m;
@@ -146,10 +173,10 @@ __device__ __forceinline__ int64_t floor_sum(uint32_t n, uint32_t m, uint32_t a,
       s += static_cast<int64_t>(n) * (b / m);
       b %= m;
     }
-    const uint64_t y = static_cast<uint64_t>(a) * n + b;
+    const uint32_t y = a * n + b;
     if (y < m) break;
-    n = static_cast<uint32_t>(y / m);
-    b = static_cast<uint32_t>(y % m);
+    n = y / m;
+    b = y % m;
     const uint32_t t = m;
     m = a;
     a = t;
@@ -212,12 +239,13 @@ __device__ __forceinline__ int64_t pa_units(const PrefillParams& p, const PaSeq&
     u += pa_chunks(s.n);
     --full;
   }
-  return u + floor_sum(static_cast<uint32_t>(full), kPaChunk,
-                       static_cast<uint32_t>(p.tok_per_item),
+  return u + floor_sum(static_cast<uint32_t>(full), static_cast<uint32_t>(p.tok_per_item),
                        static_cast<uint32_t>(s.off) + p.tok_per_item + (kPaChunk - 1));
 }
 
-// The walk over a CTA's items, the same in every thread.
+// The walk over a CTA's items.  kDual: the ring is deep enough for chunks of
+// both tiles' own (head_dim 64).
+template <bool kDual>
 struct PaWalk {
   int64_t lo, hi, u;  // the CTA's units; the current item's first unit
   int32_t b, h, i;    // sequence, KV head, item of the head
@@ -262,7 +290,7 @@ struct PaWalk {
   // t takes every other chunk from j0 + t, and tile 0 folds the two at the
   // end.
   __device__ __forceinline__ bool dual(const PrefillParams& p) const {
-    return p.allow_dual && nt <= p.tok_per_tile && j1 - j0 >= 2;
+    return kDual && nt <= p.tok_per_tile && j1 - j0 >= 2;
   }
   // the end of tile t's chunks: past its last row's limit there are none
   __device__ __forceinline__ int32_t tile_end(const PrefillParams& p, int t) const {
@@ -272,9 +300,18 @@ struct PaWalk {
   }
 };
 
+// floor(a b / d); a 32-bit division where the product allows (a 64-bit one
+// costs some 100 instructions).
+__device__ __forceinline__ int64_t pa_share(int64_t a, int32_t b, int32_t d) {
+  const uint64_t x = static_cast<uint64_t>(a) * static_cast<uint32_t>(b);
+  return x >> 32 ? static_cast<int64_t>(x / static_cast<uint32_t>(d))
+                 : static_cast<uint32_t>(x) / static_cast<uint32_t>(d);
+}
+
 // Every thread: the batch's units, this CTA's range and its first item.
 // Returns false when the CTA has nothing to do.
-__device__ __forceinline__ bool pa_plan(const PrefillParams& p, PaBars* bars, PaWalk& w,
+template <bool kDual>
+__device__ __forceinline__ bool pa_plan(const PrefillParams& p, PaBars* bars, PaWalk<kDual>& w,
                                         int64_t& units, int32_t& parts) {
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
   const int32_t b0 = static_cast<int32_t>(static_cast<int64_t>(p.num_seqs) * t / kPaThreads);
@@ -286,80 +323,91 @@ __device__ __forceinline__ bool pa_plan(const PrefillParams& p, PaBars* bars, Pa
     bars->first_b = -1;
   }
   __syncthreads();
-  for (int32_t b = b0; b < b1; ++b) {
-    bool bad;
-    const PaSeq s = pa_seq(p, b, bad, blockIdx.x == 0);
-    any_bad |= bad;
-    sum += pa_units(p, s, s.items) * p.num_kv_heads;
-  }
-  if (any_bad) bars->bad = 1;
-  int64_t incl = sum;
-#pragma unroll
-  for (int d = 1; d < 32; d *= 2) {
-    const int64_t x = __shfl_up_sync(0xffffffffu, incl, d);
-    if (lane >= d) incl += x;
-  }
-  if (lane == 31) bars->scan[warp] = incl;
-  __syncthreads();
-  int64_t before = 0, total = 0;
-#pragma unroll
-  for (int i = 0; i < kPaWarps; ++i) {
-    const int64_t x = bars->scan[i];
-    before += i < warp ? x : 0;
-    total += x;
-  }
-  units = total;
-  // no more ranges than two units each: a one-chunk item stays whole
-  const int64_t most = total / (kPaItemCost + 1);
-  parts = static_cast<int32_t>(most < p.num_ctas ? (most < 1 ? 1 : most) : p.num_ctas);
+  // pass 0 sums this thread's sequences; pass 1, after the sums over all
+  // threads, lets the thread whose sequences hold the CTA's first unit find
+  // its sequence (one copy of the code for both)
   const int32_t c = blockIdx.x;
-  w.lo = c < parts ? total * c / parts : total;
-  w.hi = c < parts ? total * (c + 1) / parts : total;
-  const bool go = !bars->bad && w.lo < w.hi;
-  int64_t at = before + incl - sum;
-  if (go && at <= w.lo && w.lo < at + sum) {
-    for (int32_t b = b0; b < b1; ++b) {
-      bool bad;
-      const PaSeq s = pa_seq(p, b, bad, false);
-      const int64_t x = pa_units(p, s, s.items) * p.num_kv_heads;
-      if (w.lo < at + x) {
-        bars->first_b = b;
-        bars->first_u = at;
-        break;
+  int64_t at = 0;  // units before the thread's sequences
+  bool go = true;
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+    if (pass == 0 || (go && at <= w.lo && w.lo < at + sum)) {
+#pragma unroll 1
+      for (int32_t b = b0; b < b1; ++b) {
+        bool bad;
+        const PaSeq s = pa_seq(p, b, bad, pass == 0 && c == 0);
+        any_bad |= bad;
+        const int64_t x = pa_units(p, s, s.items) * p.num_kv_heads;
+        if (pass == 0) {
+          sum += x;
+        } else {
+          if (w.lo < at + x) {
+            bars->first_b = b;
+            bars->first_u = at;
+            break;
+          }
+          at += x;
+        }
       }
-      at += x;
     }
+    if (pass == 1) break;
+    if (any_bad) bars->bad = 1;
+    int64_t incl = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const int64_t x = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += x;
+    }
+    if (lane == 31) bars->scan[warp] = incl;
+    __syncthreads();
+    int64_t before = 0, total = 0;
+#pragma unroll
+    for (int i = 0; i < kPaWarps; ++i) {
+      const int64_t x = bars->scan[i];
+      before += i < warp ? x : 0;
+      total += x;
+    }
+    units = total;
+    // no more ranges than two units each: a one-chunk item stays whole
+    const int64_t most = total / (kPaItemCost + 1);
+    parts = static_cast<int32_t>(most < p.num_ctas ? (most < 1 ? 1 : most) : p.num_ctas);
+    w.lo = c < parts ? pa_share(total, c, parts) : total;
+    w.hi = c < parts ? pa_share(total, c + 1, parts) : total;
+    go = !bars->bad && w.lo < w.hi;
+    at = before + incl - sum;
   }
   __syncthreads();
-  if (!go) return false;
+  if (!go || bars->first_b < 0) return false;
+  // the CTA's first item: the KV head, then the head's last item that starts
+  // at or before the rest of the units, 32 candidates a round
   w.b = bars->first_b;
-  if (w.b < 0) return false;
   bool bad;
   w.s = pa_seq(p, w.b, bad, false);
-  const int64_t per_head = pa_units(p, w.s, w.s.items);
-  const int64_t x = w.lo - bars->first_u;
-  w.h = static_cast<int32_t>(x / per_head);
-  const int64_t y = x - w.h * per_head;
-  // the last item that starts at or before y, 32 candidates a round
+  int64_t y = w.lo - bars->first_u, start = 0;
   int32_t a = 0, e = w.s.items;
-  while (e - a > 1) {
+  w.u = bars->first_u;
+#pragma unroll 1
+  for (bool head = true; head || e - a > 1; head = false) {
     const int32_t step = (e - a + 31) / 32;
-    const int64_t k = a + static_cast<int64_t>(lane) * step;
-    const bool le = k < e && pa_units(p, w.s, static_cast<int32_t>(k)) <= y;
-    const uint32_t m = __ballot_sync(0xffffffffu, le);
-    a += (31 - __clz(m)) * step;  // lane 0 always holds
+    const int64_t k = head ? e : a + static_cast<int64_t>(lane) * step;
+    const int64_t before = pa_units(p, w.s, static_cast<int32_t>(k < e ? k : e));
+    if (head) {  // units of one KV head
+      w.h = y >> 32 || before >> 32
+                ? static_cast<int32_t>(y / before)
+                : static_cast<int32_t>(static_cast<uint32_t>(y) / static_cast<uint32_t>(before));
+      y -= w.h * before;
+      w.u += w.h * before;
+      continue;
+    }
+    const int last = 31 - __clz(__ballot_sync(0xffffffffu, k < e && before <= y));
+    start = __shfl_sync(0xffffffffu, before, last);  // lane 0 always qualifies
+    a += last * step;
     e = min(e, a + step);
   }
   w.i = a;
-  w.u = bars->first_u + w.h * per_head + pa_units(p, w.s, a);
+  w.u += start;
   w.item(p);
   return true;
-}
-
-// Byte offset of 16-byte chunk c (along the row's D * 2 bytes) of row r in
-// a query tile stored as 128-byte slabs (128-byte swizzle).
-__device__ __forceinline__ uint32_t pa_q_chunk(int r, int c) {
-  return (c >> 3) * (kPaRows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
 }
 
 // 4D tiled TMA load of one box into shared memory, completing on `bar`.
@@ -405,7 +453,7 @@ struct PaItems {
   uint32_t k = 0;
   // the next record; NULL after a failed wait
   __device__ __forceinline__ const PaItem* get(PaBars* bars) {
-    const bool ok = mbar_wait(smem_addr(&bars->item_full[k % kPaItems]), (k / kPaItems) & 1);
+    const bool ok = pa_wait(smem_addr(&bars->item_full[k % kPaItems]), (k / kPaItems) & 1);
     return __all_sync(0xffffffffu, ok) ? &bars->item[k % kPaItems] : nullptr;
   }
   // the warp has read it
@@ -416,17 +464,17 @@ struct PaItems {
   }
 };
 
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
+// A position in the ring: its stage and the parity of its current use.
+template <int kStages>
+struct PaRing {
+  uint32_t stage = 0, phase = 0;
+  __device__ __forceinline__ void advance() {
+    if (++stage == kStages) {
+      stage = 0;
+      phase ^= 1u;
+    }
+  }
+};
 
 template <int kRegs>
 __device__ __forceinline__ void regs_dec() {
@@ -465,7 +513,7 @@ __device__ __forceinline__ void pa_copies(const PrefillParams& p, PaBars* bars,
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
         const uint32_t st = slot % L::kStages, use = slot / L::kStages;
-        if (use > 0) ok = mbar_wait(smem_addr(&bars->empty[st]), (use - 1) & 1);
+        if (use > 0) ok = pa_wait(smem_addr(&bars->empty[st]), (use - 1) & 1);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         const uint32_t bar = smem_addr(&bars->full[st]);
@@ -483,17 +531,17 @@ __device__ __forceinline__ void pa_copies(const PrefillParams& p, PaBars* bars,
   // normal path the MMAs have consumed every one already.
   if (lane == 0)
     for (uint32_t k = slot < L::kStages ? 0 : slot - L::kStages; k < slot; ++k)
-      mbar_wait(smem_addr(&bars->full[k % L::kStages]), (k / L::kStages) & 1, 1u << 16);
+      pa_wait(smem_addr(&bars->full[k % L::kStages]), (k / L::kStages) & 1, 1u << 16);
 }
 
-// Warp 2: walks the CTA's items, hands each to the other warps, and loads
+// Warp 1: walks the CTA's items, hands each to the other warps, and loads
 // its query rows into each tile as soon as the item before has done its last
 // score product of that tile: the next item's scores start behind its last
 // P.V product.  One 4D box per 64-column slab: 64 columns x G heads x the
 // tile's tokens.  Tokens past the item are the next sequence's (or zeros
 // past the batch): rows that are never stored.
 template <int D>
-__device__ __forceinline__ void pa_items(const PrefillParams& p, PaBars* bars, PaWalk& w,
+__device__ __forceinline__ void pa_items(const PrefillParams& p, PaBars* bars, PaWalk<PaSmem<D>::kDual>& w,
                                          const CUtensorMap* tm_q, uint32_t sq, int64_t units,
                                          int32_t parts) {
   using L = PaSmem<D>;
@@ -505,7 +553,7 @@ __device__ __forceinline__ void pa_items(const PrefillParams& p, PaBars* bars, P
   uint32_t raw = 0;         // tiles that took the way over q_raw
   bool ok = true;
   auto publish = [&](const PaItem& it) {
-    if (k >= kPaItems) ok = mbar_wait(smem_addr(&bars->item_empty[k % kPaItems]), (k / kPaItems - 1) & 1);
+    if (k >= kPaItems) ok = pa_wait(smem_addr(&bars->item_empty[k % kPaItems]), (k / kPaItems - 1) & 1);
     ok = __all_sync(0xffffffffu, ok);
     if (!ok) return;
     if (lane == 0) {
@@ -531,34 +579,35 @@ __device__ __forceinline__ void pa_items(const PrefillParams& p, PaBars* bars, P
     it.flags = (whole ? kPaWhole : 0) | (w.dual(p) ? kPaDual : 0) | (w.j0 == 0 ? kPaHead : 0);
     // the CTA that holds the item's last unit
     const int64_t x = w.u + kPaItemCost + w.chunks;
-    it.job = whole ? -1 : static_cast<int32_t>((x * parts - 1) / units);
+    const uint64_t z = static_cast<uint64_t>(x) * static_cast<uint32_t>(parts) - 1;
+    it.job = whole ? -1
+             : z >> 32 || units >> 32
+                 ? static_cast<int32_t>(z / static_cast<uint64_t>(units))
+                 : static_cast<int32_t>(static_cast<uint32_t>(z) / static_cast<uint32_t>(units));
     return it;
   };
-  while (!w.done() && !w.mine) w.next(p);
   PaItem it = {};
-  bool have = !w.done();
-  if (have)
-    it = record();
-  else
-    it.flags = kPaEnd;
-  publish(it);
-  while (have && ok) {
-    // the record behind this item first: the copies run ahead into it
+  bool first = true;
+  while (ok && !(it.flags & kPaEnd)) {
+    // the record behind an item goes out before its queries: the copies run
+    // ahead into it
     const PaItem cur = it;
-    do w.next(p);
-    while (!w.done() && !w.mine);
-    have = !w.done();
-    if (have)
-      it = record();
-    else
+    while (!w.done()) {
+      if (!first) w.next(p);
+      first = false;
+      if (w.done() || w.mine) break;
+    }
+    if (w.done())
       it.flags = kPaEnd;
+    else
+      it = record();
     publish(it);
-    if (!ok || cur.j1 <= cur.j0) continue;
+    if (!ok || cur.j1 <= cur.j0) continue;  // no chunks (or nothing before): no queries
 #pragma unroll 1
     for (int t = 0; t < kPaTiles; ++t) {
       if ((t == 0 ? cur.end[0] : cur.end[1]) <= cur.j0) continue;
       if (loaded >> t & 1u) {
-        ok = mbar_wait(smem_addr(&bars->q_free[t]), phase >> t & 1u);
+        ok = pa_wait(smem_addr(&bars->q_free[t]), phase >> t & 1u);
         phase ^= 1u << t;
       }
       ok = __all_sync(0xffffffffu, ok);
@@ -576,7 +625,7 @@ __device__ __forceinline__ void pa_items(const PrefillParams& p, PaBars* bars, P
       __syncwarp();
       if (plain) continue;
       // a negative or zero scale: the words are changed in place
-      ok = mbar_wait(bar, raw++ & 1);
+      ok = pa_wait(bar, raw++ & 1);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       for (uint32_t i = lane * 16; i < L::kQ; i += 512) {
@@ -600,160 +649,145 @@ __device__ __forceinline__ void pa_items(const PrefillParams& p, PaBars* bars, P
   if (lane == 0 && plain)
     for (int t = 0; t < kPaTiles; ++t)
       if (loaded >> t & 1u)
-        mbar_wait(smem_addr(&bars->q_full[t]), phase >> t & 1u, 1u << 16);
+        pa_wait(smem_addr(&bars->q_full[t]), phase >> t & 1u, 1u << 16);
 }
 
-// Warp 1, lane 0 issuing: per chunk j and tile t, once the softmax has
-// written P_j over S_j:
-//     O_t += P_j . V_j    (P in tensor memory, V MN-major; N = D)
-//     S_t  = Q_t . K_j'^T (the tile's next chunk; both K-major; N = 128)
+// Warps 2 and 3, one thread each: tile t's products.  Per chunk j of the
+// tile, once the softmax has written P_j over S_j:
+//     O += P_j . V_j     (P in tensor memory, V MN-major; N = D)
+//     S  = Q . K_j'^T    (the tile's next chunk; both K-major; N = 128)
 // in that order: one thread's MMAs run in issue order, so the new scores
 // land in P_j's columns only after the product has read them, and their
-// completion also means the product is done.  The tiles alternate, so one's
-// softmax runs beside the other's MMAs.  The tensor pipe holds some 300
-// cycles of issued MMAs: what this warp waits for between two tiles' groups
-// stays below that (one wait, for P; the next chunk's copies are looked at
-// beforehand, between the tiles).
+// completion also means the product is done.
+//
+// The tensor pipe takes an MMA of this shape every 64 cycles but queues only
+// one or two, and every wait on a barrier costs its thread 100 to 200: with
+// one thread for both tiles the pipe ran dry for some 700 cycles between
+// two tiles' 1024 (measured with time stamps).  So each tile has its own
+// thread, which goes through its waits while the other issues.  While both
+// tiles have chunks left the threads take turns, 16 MMAs each: interleaved,
+// both tiles' MMAs would end together, and both softmaxes and then both
+// products would run at the same time for good; one after the other they
+// stay half a period apart.
+//
+// A stage is free once both threads have passed it; for chunks of the other
+// tile (dual items, causal tiles that end earlier) this one only arrives,
+// in ring order.
 template <int D>
-__device__ __forceinline__ void pa_mma(const PrefillParams& p, PaBars* bars, uint32_t tmem,
+__device__ __forceinline__ void pa_mma(const PrefillParams& p, PaBars* bars, int t, uint32_t tmem,
                                        uint32_t sq, uint32_t ring) {
   using L = PaSmem<D>;
   constexpr uint32_t kIdQK = idesc_bf16(kPaRows, kPaChunk, false, false);
   constexpr uint32_t kIdPV = idesc_bf16(kPaRows, D, false, true);
   const bool leader = (threadIdx.x & 31) == 0;
+  const uint32_t tt = tmem + t * kPaTileCols;
+  const uint32_t qb = sq + t * L::kQ;
   PaItems items;
-  uint32_t slot0 = 0;                        // ring slot of the item's first K
-  uint32_t qph = 0, pph = 0;  // bit t: parity of tile t's next queries, next P
+  PaRing<L::kStages> r;
+  uint32_t qph = 0, pph = 0, tph = 0;  // parity of the next queries, P, turn
+  bool owed = false;  // a turn of the other tile's that this one has not waited for
   bool ok = true;
-  auto wait = [&](uint64_t* bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, mbar_wait(smem_addr(bar), parity));
+  auto full = [&]() { return pa_wait(smem_addr(&bars->full[r.stage]), r.phase); };
+  // the stage of a chunk that is not this tile's
+  auto pass = [&]() {
+    ok = ok && full();
+    if (ok) mbar_arrive(smem_addr(&bars->empty[r.stage]));
+    r.advance();
   };
-  auto queries = [&](int t) {
-    const bool got = wait(&bars->q_full[t], qph >> t & 1u);
-    qph ^= 1u << t;
-    return got;
-  };
-  auto weights = [&](int t) {
-    const bool got = wait(&bars->p_full[t], pph >> t & 1u);
-    pph ^= 1u << t;
-    return got;
-  };
-  auto landed = [&](uint32_t slot) {
-    return wait(&bars->full[slot % L::kStages], (slot / L::kStages) & 1);
-  };
-  auto there = [&](uint32_t slot) {
-    return mbar_test(smem_addr(&bars->full[slot % L::kStages]), (slot / L::kStages) & 1);
-  };
-  auto scores = [&](int t, uint32_t slot, bool last) {
-    if (leader) {
-      const uint32_t qb = sq + t * L::kQ, kb = ring + (slot % L::kStages) * L::kKV;
+  auto scores = [&](uint32_t st) {
+    const uint32_t kb = ring + st * L::kKV;
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k)
-        umma_bf16(tmem + t * kPaTileCols + kPaSCol,
-                  smem_desc_sw128(qb + (k >> 2) * (kPaRows * 128) + (k & 3) * 32, 16, 1024),
-                  smem_desc_sw128(kb + (k >> 2) * 1024 + (k & 3) * 32, 16, L::kGroup), kIdQK,
-                  k > 0);
-      umma_commit(smem_addr(&bars->s_full[t]));
-      if (last) umma_commit(smem_addr(&bars->q_free[t]));
-    }
-    __syncwarp();
+    for (int k = 0; k < D / 16; ++k)
+      umma_bf16(tt + kPaSCol,
+                smem_desc_sw128(qb + (k >> 2) * (kPaRows * 128) + (k & 3) * 32, 16, 1024),
+                smem_desc_sw128(kb + (k >> 2) * 1024 + (k & 3) * 32, 16, L::kGroup), kIdQK, k > 0);
   };
-  auto product = [&](int t, uint32_t slot, bool first) {
-    if (leader) {
-      const uint32_t tt = tmem + t * kPaTileCols, vb = ring + (slot % L::kStages) * L::kKV;
-#pragma unroll
-      for (int k = 0; k < kPaChunk / 16; ++k)
-        umma_bf16_ta(tt + kPaOCol, tt + kPaSCol + k * 8,
-                     smem_desc_sw128(vb + k * 2 * L::kGroup, 1024, L::kGroup), kIdPV,
-                     !first || k > 0);
-    }
-    __syncwarp();
-  };
-  auto release = [&](uint32_t slot) {
-    if (leader) umma_commit(smem_addr(&bars->empty[slot % L::kStages]));
-    __syncwarp();
-  };
-  auto last_of = [&](int t) {
-    if (leader) umma_commit(smem_addr(&bars->o_last[t]));
-    __syncwarp();
-  };
-  while (ok) {
+  while (true) {
     const PaItem* it = items.get(bars);
     if (it == nullptr || (it->flags & kPaEnd)) break;
-    const int32_t j0 = it->j0, j1 = it->j1, end0 = it->end[0], end1 = it->end[1];
-    const bool dual = it->flags & kPaDual;
-    items.put(bars);
-    if (j1 <= j0) continue;
-    // chunk j: K in slot at(j), V behind it
-    auto at = [&](int32_t j) { return slot0 + 2u * static_cast<uint32_t>(j - j0); };
-    if (dual) {
-      // tile t has chunks j0 + t, j0 + t + 2, ...
-      for (int t = 0; t < 2 && ok; ++t) {
-        ok = landed(at(j0 + t)) && queries(t);
-        if (!ok) break;
-        tc_fence_after_sync();
-        scores(t, at(j0 + t), j0 + t + 2 >= j1);
-        release(at(j0 + t));
+    if (leader && it->j1 > it->j0) {
+      const int32_t j0 = it->j0, j1 = it->j1, end0 = it->end[0], end1 = it->end[1];
+      const int32_t end = t == 0 ? end0 : end1;
+      const bool dual = L::kDual && (it->flags & kPaDual);
+      const int32_t step = dual ? 2 : 1;
+      // turns of the item: chunks that both tiles have
+      const int32_t both = dual ? (j1 - j0) / 2 : min(end0, end1) - j0;
+      int32_t j = j0;
+      if (dual && t == 1) {
+        pass();
+        pass();
+        ++j;
       }
-      for (int32_t j = j0; j < j1 && ok; ++j) {
-        const int t = (j - j0) & 1;
-        ok = landed(at(j) + 1) && weights(t);
-        if (!ok) break;
-        tc_fence_after_sync();
-        product(t, at(j) + 1, j - t == j0);
-        if (j + 2 < j1) {
-          ok = landed(at(j + 2));
-          if (!ok) break;
+      if (j < end && ok) {
+        ok = full() && pa_wait(smem_addr(&bars->q_full[t]), qph);
+        qph ^= 1u;
+        if (ok) {
           tc_fence_after_sync();
-          scores(t, at(j + 2), j + 4 >= j1);
-          release(at(j + 2));
-        } else {
-          last_of(t);
+          scores(r.stage);
+          umma_commit(smem_addr(&bars->s_full[t]));
+          umma_commit(smem_addr(&bars->empty[r.stage]));
+          if (j + step >= end) umma_commit(smem_addr(&bars->q_free[t]));
+          r.advance();
         }
-        release(at(j) + 1);
       }
-    } else {
-      ok = landed(at(j0));
-      for (int t = 0; t < 2 && ok; ++t) {
-        if ((t == 0 ? end0 : end1) <= j0) continue;
-        ok = queries(t);
+      for (int32_t n = 0; j < end && ok; j += step, ++n) {
+        const bool more = j + step < end;
+        ok = full();
+        const uint32_t vst = r.stage, vb = ring + vst * L::kKV;
+        r.advance();
+        if (more) {
+          if (dual) {  // the other tile's chunk lies between
+            pass();
+            pass();
+          }
+          ok = ok && full();
+        }
+        ok = ok && pa_wait(smem_addr(&bars->p_full[t]), pph);
+        pph ^= 1u;
+        // tile 0's turn n comes behind tile 1's n - 1, tile 1's behind tile 0's n
+        if (ok && (owed || (t == 0 ? n >= 1 && n <= both : n < both))) {
+          ok = pa_wait(smem_addr(&bars->turn[t]), tph);
+          tph ^= 1u;
+          owed = false;
+        }
         if (!ok) break;
         tc_fence_after_sync();
-        scores(t, at(j0), j0 + 1 >= (t == 0 ? end0 : end1));
-      }
-      if (ok) release(at(j0));
-      bool ready = false;  // V_j and K_j+1 have been seen to have landed
-      for (int32_t j = j0; j < j1 && ok; ++j) {
-        const uint32_t vs = at(j) + 1, ks = at(j + 1);
-        if (!ready) ok = landed(vs) && (j + 1 >= j1 || landed(ks));
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const int32_t end = t == 0 ? end0 : end1;
-          if (ok && j < end) {
-            ok = weights(t);
-            if (ok) {
-              tc_fence_after_sync();
-              product(t, vs, j == j0);
-              if (j + 1 < end)
-                scores(t, ks, j + 2 >= end);
-              else
-                last_of(t);
-            }
-          }
-          if (t == 0 && ok && j + 1 < j1)
-            ready = __all_sync(0xffffffffu, there(ks + 1) && (j + 2 >= j1 || there(at(j + 2))));
+        for (int k = 0; k < kPaChunk / 16; ++k)
+          umma_bf16_ta(tt + kPaOCol, tt + kPaSCol + k * 8,
+                       smem_desc_sw128(vb + k * 2 * L::kGroup, 1024, L::kGroup), kIdPV,
+                       n > 0 || k > 0);
+        if (more) scores(r.stage);
+        if (n < both) mbar_arrive(smem_addr(&bars->turn[1 - t]));
+        if (more) {
+          umma_commit(smem_addr(&bars->s_full[t]));
+          if (j + 2 * step >= end) umma_commit(smem_addr(&bars->q_free[t]));
+          umma_commit(smem_addr(&bars->empty[vst]));
+          umma_commit(smem_addr(&bars->empty[r.stage]));
+          r.advance();
+        } else {
+          umma_commit(smem_addr(&bars->o_last[t]));
+          umma_commit(smem_addr(&bars->empty[vst]));
         }
-        if (!ok) break;
-        release(vs);
-        if (j + 1 < j1) release(ks);
+      }
+      // tile 1's last turn, where tile 0 has no further chunk of its own
+      if (t == 0 && both > 0 && end - j0 <= both * step) owed = true;
+      // chunks behind the tile's last one
+      if (dual) j -= 1;
+      for (; j < j1 && ok; ++j) {
+        pass();
+        pass();
       }
     }
-    slot0 += 2u * static_cast<uint32_t>(j1 - j0);
+    ok = __shfl_sync(0xffffffffu, ok, 0);
+    if (!ok) break;
+    items.put(bars);
   }
-  // every MMA issued has completed before the tensor memory is released
+  // every MMA this thread issued has completed before the tensor memory is
+  // released
   if (leader) {
-    umma_commit(smem_addr(&bars->mma_done));
-    mbar_wait(smem_addr(&bars->mma_done), 0, 1u << 16);
+    umma_commit(smem_addr(&bars->mma_done[t]));
+    pa_wait(smem_addr(&bars->mma_done[t]), 0, 1u << 16);
   }
   __syncwarp();
 }
@@ -830,7 +864,7 @@ __device__ __forceinline__ void pa_softmax(const PrefillParams& p, PaBars* bars,
   while (ok) {
     const PaItem* it = items.get(bars);
     if (it == nullptr || (it->flags & kPaEnd)) break;
-    const bool dual = it->flags & kPaDual;
+    const bool dual = L::kDual && (it->flags & kPaDual);
     const int32_t j0 = it->j0, begin = j0 + (dual ? tile : 0), step = dual ? 2 : 1;
     const int32_t end = it->end[tile], n = it->n;
     const int32_t tk = rt + (dual ? 0 : tile * p.tok_per_tile);  // the row's token of the item
@@ -842,7 +876,7 @@ __device__ __forceinline__ void pa_softmax(const PrefillParams& p, PaBars* bars,
     float2 la = make_float2(0.f, 0.f);
 #pragma unroll 1
     for (int32_t j = begin; j < end; j += step) {
-      ok = mbar_wait(smem_addr(&bars->s_full[tile]), sn++ & 1);
+      ok = pa_wait(smem_addr(&bars->s_full[tile]), sn++ & 1);
       if (!__all_sync(0xffffffffu, ok)) {
         ok = false;
         break;
@@ -915,7 +949,7 @@ __device__ __forceinline__ void pa_softmax(const PrefillParams& p, PaBars* bars,
       const int32_t past = n - j * kPaChunk;  // valid tokens of the chunk
       if (past < kPaChunk) {
         const uint32_t slot = 2 * (cc + static_cast<uint32_t>(j - j0)) + 1;
-        ok = mbar_wait(smem_addr(&bars->full[slot % L::kStages]), (slot / L::kStages) & 1);
+        ok = pa_wait(smem_addr(&bars->full[slot % L::kStages]), (slot / L::kStages) & 1);
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
           break;
@@ -939,7 +973,7 @@ __device__ __forceinline__ void pa_softmax(const PrefillParams& p, PaBars* bars,
       if (lane == 0) mbar_arrive(smem_addr(&bars->p_full[tile]));
     }
     if (end > begin && ok) {
-      ok = mbar_wait(smem_addr(&bars->o_last[tile]), on++ & 1);
+      ok = pa_wait(smem_addr(&bars->o_last[tile]), on++ & 1);
       ok = __all_sync(0xffffffffu, ok);
     }
     if (!ok) break;
@@ -953,12 +987,12 @@ __device__ __forceinline__ void pa_softmax(const PrefillParams& p, PaBars* bars,
         __syncwarp();
         tc_fence_before_sync();
         if (lane == 0) mbar_arrive(smem_addr(&bars->ml_full));
-        ok = mbar_wait(smem_addr(&bars->o_free), dn++ & 1);
+        ok = pa_wait(smem_addr(&bars->o_free), dn++ & 1);
         ok = __all_sync(0xffffffffu, ok);
         items.put(bars);
         continue;
       }
-      ok = mbar_wait(smem_addr(&bars->ml_full), dn++ & 1);
+      ok = pa_wait(smem_addr(&bars->ml_full), dn++ & 1);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after_sync();
@@ -1049,7 +1083,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::kStages; ++i) {
       mbar_init(smem_addr(&bars->full[i]), 1);
-      mbar_init(smem_addr(&bars->empty[i]), 1);
+      mbar_init(smem_addr(&bars->empty[i]), kPaTiles);
     }
     for (int t = 0; t < kPaTiles; ++t) {
       mbar_init(smem_addr(&bars->q_full[t]), 1);
@@ -1057,12 +1091,13 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       mbar_init(smem_addr(&bars->s_full[t]), 1);
       mbar_init(smem_addr(&bars->p_full[t]), 4);
       mbar_init(smem_addr(&bars->o_last[t]), 1);
+      mbar_init(smem_addr(&bars->turn[t]), 1);
+      mbar_init(smem_addr(&bars->mma_done[t]), 1);
     }
     for (int i = 0; i < kPaItems; ++i) {
       mbar_init(smem_addr(&bars->item_full[i]), 1);
-      mbar_init(smem_addr(&bars->item_empty[i]), 2 + kPaTiles * 4);
+      mbar_init(smem_addr(&bars->item_empty[i]), 1 + kPaTiles * 5);
     }
-    mbar_init(smem_addr(&bars->mma_done), 1);
     mbar_init(smem_addr(&bars->q_raw), 1);
     mbar_init(smem_addr(&bars->ml_full), 4);
     mbar_init(smem_addr(&bars->o_free), 4);
@@ -1082,7 +1117,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   pdl_wait();  // launched as a programmatic dependent: inputs ready below
   pdl_trigger();
 
-  PaWalk w;
+  PaWalk<L::kDual> w;
   int64_t units;
   int32_t parts;
   const bool work = pa_plan(p, bars, w, units, parts);
@@ -1094,9 +1129,9 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     if (warp == 0)
       pa_copies<D>(p, bars, &tm_k, &tm_v, ring);
     else if (warp == 1)
-      pa_mma<D>(p, bars, tmem, sq, ring);
-    else if (warp == 2)
       pa_items<D>(p, bars, w, &tm_q, sq, units, parts);
+    else
+      pa_mma<D>(p, bars, warp - 2, tmem, sq, ring);
   } else {
     regs_inc<kPaRegsSoft>();
     pa_softmax<D>(p, bars, (warp - kPaSoftWarp) >> 2, tmem, ring,

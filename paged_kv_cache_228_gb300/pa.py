@@ -491,30 +491,48 @@ def pa_decode_noalloc(q, k_cache, v_cache, block_tables, seq_lens, scale, out,
 
 
 # ----------------------------------------------------------- prompt side ---
-def _same_device(*named):
-    """The one CUDA device of the given (name, tensor or None) pairs.  Unlike
-    the decode calls, the prompt-side calls may be made while another device
-    is current: they run on their tensors' device."""
-    dev = None
-    for name, t in named:
-        if t is None:
-            continue
-        if t.device.type != "cuda":
-            raise ValueError(f"{name}: must be a CUDA tensor, is on {t.device}")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"{name}: is on {t.device}, the others on {dev}")
+# These calls are made between short kernels, so their checks are kept to a
+# few attribute reads per tensor: 4 us instead of 20 us a call on a Grace
+# core.  Unlike the decode calls, they may be made while another device is
+# current: they run on their tensors' device.
+def _bad(t, name, dtype, shape):
+    """Why `t` is not a contiguous `dtype` tensor of `shape`."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.dim() != len(shape) or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name}: must be contiguous")
+
+
+def _device_of(tensors, names):
+    """The index of the one CUDA device that all tensors (None: absent) are on."""
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev or dev < 0:
+            for t, name in zip(tensors, names):
+                if t is not None and t.get_device() < 0:
+                    raise ValueError(f"{name}: must be a CUDA tensor, is on {t.device}")
+            raise ValueError("tensors on different devices: " + ", ".join(
+                f"{name} on {t.device}" for t, name in zip(tensors, names) if t is not None))
     return dev
 
 
-def _stream_of(stream, dev):
-    return _stream(torch.cuda.current_stream(dev) if stream is None else stream)
+def _call(fn, dev, stream, args):
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+    elif isinstance(stream, torch.cuda.Stream):
+        stream = stream.cuda_stream
+    if torch._C._cuda_getDevice() == dev:
+        status = getattr(_lib or lib(), fn)(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            status = getattr(_lib or lib(), fn)(*args, stream)
+    if status != PA_OK:
+        raise PAError(fn, status)
 
 
-def _shape(t, shape, name):
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+_APPEND = ("lens", "n_new", "block_tables", "free_ids", "num_free", "slot_mapping", "q_start",
+           "seq_lens", "num_free_out", "num_done")
 
 
 def pa_append_slots_device(lens, n_new, block_tables, free_ids, num_free, block_size,
@@ -524,28 +542,25 @@ def pa_append_slots_device(lens, n_new, block_tables, free_ids, num_free, block_
     the query offsets q_start [B + 1] and seq_lens.  seq_lens may be lens,
     num_free_out may be num_free.  len(slot_mapping) is the token capacity
     (rows past the last sequence get -1)."""
-    B = lens.shape[0]
-    for t, name, n in ((lens, "lens", B), (n_new, "n_new", B), (free_ids, "free_ids", None),
-                       (num_free, "num_free", 1), (q_start, "q_start", B + 1),
-                       (seq_lens, "seq_lens", B), (num_free_out, "num_free_out", 1),
-                       (num_done, "num_done", 1)):
-        _need(t, torch.int32, name, 1)
-        if n is not None:
-            _shape(t, (n,), name)
-    _need(block_tables, torch.int32, "block_tables", 2)
-    _shape(block_tables, (B, block_tables.shape[1]), "block_tables")
-    _need(slot_mapping, torch.int64, "slot_mapping", 1)
-    dev = _same_device(("lens", lens), ("n_new", n_new), ("block_tables", block_tables),
-                       ("free_ids", free_ids), ("num_free", num_free),
-                       ("slot_mapping", slot_mapping), ("q_start", q_start),
-                       ("seq_lens", seq_lens), ("num_free_out", num_free_out),
-                       ("num_done", num_done))
-    with torch.cuda.device(dev):
-        _check("pa_append_slots_device", lib().pa_append_slots_device(
-            _ptr(lens), _ptr(n_new), _ptr(block_tables), block_tables.shape[1], _ptr(free_ids),
-            _ptr(num_free), B, slot_mapping.shape[0], block_size, free_ids.shape[0],
-            _ptr(slot_mapping), _ptr(q_start), _ptr(seq_lens), _ptr(num_free_out),
-            _ptr(num_done), _stream_of(stream, dev)))
+    i32 = torch.int32
+    B, = lens.shape
+    N, = free_ids.shape
+    T, = slot_mapping.shape
+    width = block_tables.shape[-1]
+    tensors = (lens, n_new, block_tables, free_ids, num_free, slot_mapping, q_start, seq_lens,
+               num_free_out, num_done)
+    shapes = ((B,), (B,), (B, width), (N,), (1,), (T,), (B + 1,), (B,), (1,), (1,))
+    for t, shape, name in zip(tensors, shapes, _APPEND):
+        want = torch.int64 if t is slot_mapping else i32
+        if t.dtype is not want or t.shape != shape or not t.is_contiguous():
+            _bad(t, name, want, shape)
+    _call("pa_append_slots_device", _device_of(tensors, _APPEND), stream, (
+        lens.data_ptr(), n_new.data_ptr(), block_tables.data_ptr(), width, free_ids.data_ptr(),
+        num_free.data_ptr(), B, T, block_size, N, slot_mapping.data_ptr(), q_start.data_ptr(),
+        seq_lens.data_ptr(), num_free_out.data_ptr(), num_done.data_ptr()))
+
+
+_TRIM = ("lens", "new_lens", "block_tables", "free_ids", "num_free", "seq_lens", "num_free_out")
 
 
 def pa_trim_slots_device(lens, new_lens, block_tables, free_ids, num_free, block_size, seq_lens,
@@ -553,23 +568,18 @@ def pa_trim_slots_device(lens, new_lens, block_tables, free_ids, num_free, block
     """Shrink sequence b from lens[b] to new_lens[b] tokens on the GPU: its
     blocks behind the new length are pushed onto free_ids.  seq_lens may be
     lens, num_free_out may be num_free."""
-    B = lens.shape[0]
-    for t, name, n in ((lens, "lens", B), (new_lens, "new_lens", B), (free_ids, "free_ids", None),
-                       (num_free, "num_free", 1), (seq_lens, "seq_lens", B),
-                       (num_free_out, "num_free_out", 1)):
-        _need(t, torch.int32, name, 1)
-        if n is not None:
-            _shape(t, (n,), name)
-    _need(block_tables, torch.int32, "block_tables", 2)
-    _shape(block_tables, (B, block_tables.shape[1]), "block_tables")
-    dev = _same_device(("lens", lens), ("new_lens", new_lens), ("block_tables", block_tables),
-                       ("free_ids", free_ids), ("num_free", num_free), ("seq_lens", seq_lens),
-                       ("num_free_out", num_free_out))
-    with torch.cuda.device(dev):
-        _check("pa_trim_slots_device", lib().pa_trim_slots_device(
-            _ptr(lens), _ptr(new_lens), _ptr(block_tables), block_tables.shape[1],
-            _ptr(free_ids), _ptr(num_free), B, block_size, free_ids.shape[0], _ptr(seq_lens),
-            _ptr(num_free_out), _stream_of(stream, dev)))
+    B, = lens.shape
+    N, = free_ids.shape
+    width = block_tables.shape[-1]
+    tensors = (lens, new_lens, block_tables, free_ids, num_free, seq_lens, num_free_out)
+    shapes = ((B,), (B,), (B, width), (N,), (1,), (B,), (1,))
+    for t, shape, name in zip(tensors, shapes, _TRIM):
+        if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous():
+            _bad(t, name, torch.int32, shape)
+    _call("pa_trim_slots_device", _device_of(tensors, _TRIM), stream, (
+        lens.data_ptr(), new_lens.data_ptr(), block_tables.data_ptr(), width,
+        free_ids.data_ptr(), num_free.data_ptr(), B, block_size, N, seq_lens.data_ptr(),
+        num_free_out.data_ptr()))
 
 
 def pa_attention_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim,
@@ -580,45 +590,56 @@ def pa_attention_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim,
     return int(n.value)
 
 
+_ATTEND = ("q", "k_cache", "v_cache", "block_tables", "seq_lens", "out", "q_start", "workspace",
+           "k_scale", "v_scale")
+
+
 def _attention(fn, q, k_cache, v_cache, block_tables, q_start, seq_lens, scale, out, workspace,
                k_scale, v_scale, num_splits, stream):
-    _need(q, torch.bfloat16, "q", 3)
-    _need(out, torch.bfloat16, "out", 3)
-    _shape(out, q.shape, "out")
-    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        _need(t, k_cache.dtype, name, 4)
-        _shape(t, k_cache.shape, name)
-    _need(block_tables, torch.int32, "block_tables", 2)
-    _need(seq_lens, torch.int32, "seq_lens", 1)
+    bf16, i32 = torch.bfloat16, torch.int32
     T, hq, d = q.shape
     nb, hkv, bs, d2 = k_cache.shape
-    B = seq_lens.shape[0]
+    B, = seq_lens.shape
+    width = block_tables.shape[-1]
+    if q.dtype is not bf16 or not q.is_contiguous():
+        _bad(q, "q", bf16, (T, hq, d))
+    if out.dtype is not bf16 or out.shape != q.shape or not out.is_contiguous():
+        _bad(out, "out", bf16, q.shape)
+    kv = _kv_dtype(k_cache)
+    if not k_cache.is_contiguous():
+        _bad(k_cache, "k_cache", k_cache.dtype, k_cache.shape)
+    if v_cache.dtype is not k_cache.dtype or v_cache.shape != k_cache.shape or \
+            not v_cache.is_contiguous():
+        _bad(v_cache, "v_cache", k_cache.dtype, k_cache.shape)
     if d2 != d:
         raise ValueError(f"{fn}: head_dim of q is {d}, of the cache {d2}")
-    _shape(block_tables, (B, block_tables.shape[1]), "block_tables")
-    if q_start is not None:
-        _need(q_start, torch.int32, "q_start", 1)
-        _shape(q_start, (B + 1,), "q_start")
-    kv = _kv_dtype(k_cache)
+    if block_tables.dtype is not i32 or block_tables.shape != (B, width) or \
+            not block_tables.is_contiguous():
+        _bad(block_tables, "block_tables", i32, (B, width))
+    if seq_lens.dtype is not i32 or not seq_lens.is_contiguous():
+        _bad(seq_lens, "seq_lens", i32, (B,))
+    if q_start is not None and (q_start.dtype is not i32 or q_start.shape != (B + 1,) or
+                                not q_start.is_contiguous()):
+        _bad(q_start, "q_start", i32, (B + 1,))
     if kv == PA_KV_FP8_E4M3:
         for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
             if t is None:
                 raise ValueError(f"{fn}: an FP8 cache needs {name}")
-            _need(t, torch.float32, name, 2)
-            _shape(t, (nb, hkv), name)
+            if t.dtype is not torch.float32 or t.shape != (nb, hkv) or not t.is_contiguous():
+                _bad(t, name, torch.float32, (nb, hkv))
     elif k_scale is not None or v_scale is not None:
         raise ValueError(f"{fn}: a bf16 cache takes no scales")
-    dev = _same_device(("q", q), ("k_cache", k_cache), ("v_cache", v_cache),
-                       ("block_tables", block_tables), ("q_start", q_start),
-                       ("seq_lens", seq_lens), ("out", out), ("workspace", workspace),
-                       ("k_scale", k_scale), ("v_scale", v_scale))
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    with torch.cuda.device(dev):
-        _check(fn, getattr(lib(), fn)(
-            _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), kv,
-            _ptr(block_tables), block_tables.shape[1], _ptr(q_start), _ptr(seq_lens), B, T, hq,
-            hkv, d, bs, nb, float(scale), _ptr(out), _ptr(workspace), ws_bytes, num_splits,
-            _stream_of(stream, dev)))
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace: must be contiguous")
+    dev = _device_of((q, k_cache, v_cache, block_tables, seq_lens, out, q_start, workspace,
+                      k_scale, v_scale), _ATTEND)
+    _call(fn, dev, stream, (
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+        None if k_scale is None else k_scale.data_ptr(),
+        None if v_scale is None else v_scale.data_ptr(), kv, block_tables.data_ptr(), width,
+        None if q_start is None else q_start.data_ptr(), seq_lens.data_ptr(), B, T, hq, hkv, d,
+        bs, nb, float(scale), out.data_ptr(), None if workspace is None else workspace.data_ptr(),
+        0 if workspace is None else workspace.nbytes, num_splits))
 
 
 def pa_prefill(q, k_cache, v_cache, block_tables, q_start, seq_lens, scale, out, workspace=None,
