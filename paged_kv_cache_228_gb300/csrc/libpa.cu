@@ -1450,6 +1450,12 @@ pa_status attention_entry(bool causal, const void* q, const void* k_cache, const
   // a limit plus a chunk and an item stays within 32 bits
   if (static_cast<int64_t>(max_blocks_per_seq) * block_size > INT_MAX - 1024)
     return PA_ERR_UNSUPPORTED;
+  // the work split counts in 32 bits: items of a head times their chunks
+  const int64_t items = num_tokens / (kPaTiles * (kPaRows / group)) + static_cast<int64_t>(num_seqs);
+  const int64_t chunks = (static_cast<int64_t>(max_blocks_per_seq) * block_size + kPaChunk - 1) / kPaChunk;
+  if (items * num_kv_heads > INT_MAX ||
+      items * num_kv_heads * (chunks + kPaItemCost) > 0xffffffffll - (1 << 20))
+    return PA_ERR_UNSUPPORTED;
   if (q_start == nullptr && group <= kMaxG)
     return decode_entry(q, k_cache, v_cache, k_scale, v_scale, kv_dtype, block_tables,
                         max_blocks_per_seq, seq_lens, num_seqs, num_q_heads, num_kv_heads,

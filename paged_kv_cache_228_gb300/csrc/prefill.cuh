@@ -120,9 +120,6 @@ struct PaBars {
   uint64_t ml_full, o_free;   // dual items: tile 1's (m, l) written; its O read
   uint64_t turn[kPaTiles];    // the other tile's MMAs of its turn have been issued
   uint64_t mma_done[kPaTiles];
-  int64_t scan[kPaWarps];
-  int64_t first_u;            // the CTA's first sequence: units before it
-  int32_t first_b;
   int32_t bad;
   uint32_t tmem;
 };
@@ -147,30 +144,34 @@ __device__ __forceinline__ uint32_t pa_div(const PrefillParams& p, uint32_t x) {
 }
 
 // ------------------------------------------------------------- the plan ---
-// sum_{i < n} floor((a i + b) / 128), with a < 2^16 and a n + b < 2^32.
-__device__ __forceinline__ int64_t floor_sum(uint32_t n, uint32_t a, uint32_t b) {
+// sum_{i < n} floor((a i + b) / 128), with a < 2^16, a n + b and the sum below
+// 2^32.
+__device__ __forceinline__ uint32_t floor_sum(uint32_t n, uint32_t a, uint32_t b) {
   uint32_t m = 128;
+  auto pairs = [](uint32_t x) {  // x (x - 1) / 2
+    return x & 1 ? (x - 1) / 2 * x : x / 2 * (x - 1);
+  };
   if ((a & (a - 1)) == 0) {
     // a = 2^k.  From 128 on: a multiple of the divisor.  Below, with q = 128
     // / a and x = i + b / a, the terms are floor(x / q): a sum of steps.
     const int k = 31 - __clz(a);
     if (k >= 7)
-      return (static_cast<int64_t>(n) * (n - 1) / 2 << (k - 7)) + static_cast<int64_t>(n) * (b >> 7);
+      return (pairs(n) << (k - 7)) + n * (b >> 7);
     auto steps = [&](uint32_t x) {  // sum_{y < x} floor(y / q)
-      const int64_t w = x >> (7 - k), r = x - (w << (7 - k));
-      return (w * (w - 1) / 2 << (7 - k)) + w * r;
+      const uint32_t w = x >> (7 - k), r = x - (w << (7 - k));
+      return (pairs(w) << (7 - k)) + w * r;
     };
     return steps((b >> k) + n) - steps(b >> k);
   }
-  int64_t s = 0;
+  uint32_t s = 0;
 #pragma unroll 1
   while (n > 0) {  // the Euclidean recursion on (m, a)
     if (a >= m) {
-      s += static_cast<int64_t>(n) * (n - 1) / 2 * (a / m);
+      s += pairs(n) * (a / m);
       a %= m;
     }
     if (b >= m) {
-      s += static_cast<int64_t>(n) * (b / m);
+      s += n * (b / m);
       b %= m;
     }
     const uint32_t y = a * n + b;
@@ -230,10 +231,10 @@ __device__ __forceinline__ int32_t pa_chunks(int32_t limit) {
 }
 
 // Units of the first k items of one KV head of the sequence.
-__device__ __forceinline__ int64_t pa_units(const PrefillParams& p, const PaSeq& s, int32_t k) {
-  int64_t u = static_cast<int64_t>(k) * kPaItemCost;
+__device__ __forceinline__ uint32_t pa_units(const PrefillParams& p, const PaSeq& s, int32_t k) {
+  uint32_t u = k * kPaItemCost;
   if (s.n == 0 || k == 0) return u;
-  if (!p.causal) return u + static_cast<int64_t>(k) * pa_chunks(s.n);
+  if (!p.causal) return u + k * pa_chunks(s.n);
   int32_t full = k;
   if (k == s.items) {  // the last item may be short
     u += pa_chunks(s.n);
@@ -247,7 +248,7 @@ __device__ __forceinline__ int64_t pa_units(const PrefillParams& p, const PaSeq&
 // both tiles' own (head_dim 64).
 template <bool kDual>
 struct PaWalk {
-  int64_t lo, hi, u;  // the CTA's units; the current item's first unit
+  uint32_t lo, hi, u;  // the CTA's units; the current item's first unit
   int32_t b, h, i;    // sequence, KV head, item of the head
   PaSeq s;
   // of the current item
@@ -260,8 +261,8 @@ struct PaWalk {
     nt = min(p.tok_per_item, s.nq - tok);
     lim = pa_limit(p, s, tok + nt);
     chunks = pa_chunks(lim);
-    const int64_t len = chunks + kPaItemCost;
-    const int64_t a = lo > u ? lo - u : 0, e = hi - u < len ? hi - u : len;
+    const uint32_t len = chunks + kPaItemCost;
+    const uint32_t a = lo > u ? lo - u : 0, e = min(hi - u, len);
     j0 = a > kPaItemCost ? static_cast<int32_t>(a - kPaItemCost) : 0;
     j1 = e > kPaItemCost ? static_cast<int32_t>(e - kPaItemCost) : 0;
     mine = chunks == 0 ? a == 0 : j1 > j0;
@@ -300,103 +301,94 @@ struct PaWalk {
   }
 };
 
-// floor(a b / d); a 32-bit division where the product allows (a 64-bit one
-// costs some 100 instructions).
-__device__ __forceinline__ int64_t pa_share(int64_t a, int32_t b, int32_t d) {
-  const uint64_t x = static_cast<uint64_t>(a) * static_cast<uint32_t>(b);
-  return x >> 32 ? static_cast<int64_t>(x / static_cast<uint32_t>(d))
-                 : static_cast<uint32_t>(x) / static_cast<uint32_t>(d);
+// The plan, first part, every thread: the units of its sequences, thread t
+// taking [B t / 384, B (t + 1) / 384).  The launch makes sure that the whole
+// batch's units stay below 2^32.
+__device__ __forceinline__ int32_t pa_first_seq(const PrefillParams& p, int t) {
+  return static_cast<int32_t>(static_cast<int64_t>(p.num_seqs) * t / kPaThreads);
 }
 
-// Every thread: the batch's units, this CTA's range and its first item.
-// Returns false when the CTA has nothing to do.
+__device__ __forceinline__ uint32_t pa_thread_units(const PrefillParams& p, PaBars* bars) {
+  const int t = threadIdx.x;
+  uint32_t sum = 0;
+#pragma unroll 1
+  for (int32_t b = pa_first_seq(p, t), e = pa_first_seq(p, t + 1); b < e; ++b) {
+    bool bad;
+    const PaSeq s = pa_seq(p, b, bad, blockIdx.x == 0);
+    if (bad) bars->bad = 1;
+    sum += pa_units(p, s, s.items) * p.num_kv_heads;
+  }
+  return sum;
+}
+
+__device__ __forceinline__ uint32_t pa_warp_sum(uint32_t x) {  // inclusive, over lanes
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, x, d);
+    if ((threadIdx.x & 31) >= d) x += y;
+  }
+  return x;
+}
+
+// Second part, one warp: this CTA's range and its first item.  `sums`: the
+// threads' units.  Returns false when the CTA has nothing to do.
 template <bool kDual>
-__device__ __forceinline__ bool pa_plan(const PrefillParams& p, PaBars* bars, PaWalk<kDual>& w,
-                                        int64_t& units, int32_t& parts) {
-  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
-  const int32_t b0 = static_cast<int32_t>(static_cast<int64_t>(p.num_seqs) * t / kPaThreads);
-  const int32_t b1 = static_cast<int32_t>(static_cast<int64_t>(p.num_seqs) * (t + 1) / kPaThreads);
-  int64_t sum = 0;
-  bool any_bad = false;
-  if (t == 0) {
-    bars->bad = 0;
-    bars->first_b = -1;
-  }
-  __syncthreads();
-  // pass 0 sums this thread's sequences; pass 1, after the sums over all
-  // threads, lets the thread whose sequences hold the CTA's first unit find
-  // its sequence (one copy of the code for both)
-  const int32_t c = blockIdx.x;
-  int64_t at = 0;  // units before the thread's sequences
-  bool go = true;
-#pragma unroll 1
-  for (int pass = 0; pass < 2; ++pass) {
-    if (pass == 0 || (go && at <= w.lo && w.lo < at + sum)) {
-#pragma unroll 1
-      for (int32_t b = b0; b < b1; ++b) {
-        bool bad;
-        const PaSeq s = pa_seq(p, b, bad, pass == 0 && c == 0);
-        any_bad |= bad;
-        const int64_t x = pa_units(p, s, s.items) * p.num_kv_heads;
-        if (pass == 0) {
-          sum += x;
-        } else {
-          if (w.lo < at + x) {
-            bars->first_b = b;
-            bars->first_u = at;
-            break;
-          }
-          at += x;
-        }
-      }
-    }
-    if (pass == 1) break;
-    if (any_bad) bars->bad = 1;
-    int64_t incl = sum;
+__device__ __forceinline__ bool pa_plan(const PrefillParams& p, PaBars* bars,
+                                        const uint32_t* sums, PaWalk<kDual>& w, uint32_t& units,
+                                        uint32_t& parts) {
+  const int lane = threadIdx.x & 31;
+  if (bars->bad) return false;
+  // lane i holds the units of threads [12 i, 12 i + 12)
+  constexpr int kPer = kPaThreads / 32;
+  uint32_t mine = 0;
 #pragma unroll
-    for (int d = 1; d < 32; d *= 2) {
-      const int64_t x = __shfl_up_sync(0xffffffffu, incl, d);
-      if (lane >= d) incl += x;
-    }
-    if (lane == 31) bars->scan[warp] = incl;
-    __syncthreads();
-    int64_t before = 0, total = 0;
-#pragma unroll
-    for (int i = 0; i < kPaWarps; ++i) {
-      const int64_t x = bars->scan[i];
-      before += i < warp ? x : 0;
-      total += x;
-    }
-    units = total;
-    // no more ranges than two units each: a one-chunk item stays whole
-    const int64_t most = total / (kPaItemCost + 1);
-    parts = static_cast<int32_t>(most < p.num_ctas ? (most < 1 ? 1 : most) : p.num_ctas);
-    w.lo = c < parts ? pa_share(total, c, parts) : total;
-    w.hi = c < parts ? pa_share(total, c + 1, parts) : total;
-    go = !bars->bad && w.lo < w.hi;
-    at = before + incl - sum;
-  }
-  __syncthreads();
-  if (!go || bars->first_b < 0) return false;
-  // the CTA's first item: the KV head, then the head's last item that starts
-  // at or before the rest of the units, 32 candidates a round
-  w.b = bars->first_b;
-  bool bad;
-  w.s = pa_seq(p, w.b, bad, false);
-  int64_t y = w.lo - bars->first_u, start = 0;
-  int32_t a = 0, e = w.s.items;
-  w.u = bars->first_u;
+  for (int i = 0; i < kPer; ++i) mine += sums[lane * kPer + i];
+  const uint32_t incl = pa_warp_sum(mine);
+  units = __shfl_sync(0xffffffffu, incl, 31);
+  // no more ranges than two units each: a one-chunk item stays whole
+  parts = max(1u, min(units / (kPaItemCost + 1), static_cast<uint32_t>(p.num_ctas)));
+  const uint32_t c = blockIdx.x;
+  if (c >= parts) return false;
+  const uint32_t q = units / parts, rest = units - q * parts;  // floor(units c / parts)
+  w.lo = q * c + rest * c / parts;
+  w.hi = q * (c + 1) + rest * (c + 1) / parts;
+  if (w.lo >= w.hi) return false;
+  // the thread whose sequences hold unit lo
+  const int li = __ffs(__ballot_sync(0xffffffffu, w.lo < incl)) - 1;
+  uint32_t at = __shfl_sync(0xffffffffu, incl - mine, li);
+  int t = li * kPer;
 #pragma unroll 1
-  for (bool head = true; head || e - a > 1; head = false) {
+  for (; t < kPaThreads - 1 && w.lo >= at + sums[t]; ++t) at += sums[t];
+  // then its sequence and the KV head (a first round with all the items of a
+  // head), then the head's last item that starts at or before the rest y,
+  // 32 candidates a round
+  w.b = pa_first_seq(p, t);
+  uint32_t y = w.lo - at, start = 0;
+  int32_t a = 0, e = 0;
+  bool found = false;
+#pragma unroll 1
+  while (!found || e - a > 1) {
+    if (!found) {
+      if (w.b >= p.num_seqs) return false;  // lengths changed under the call
+      bool bad;
+      w.s = pa_seq(p, w.b, bad, false);
+      e = w.s.items;
+    }
     const int32_t step = (e - a + 31) / 32;
-    const int64_t k = head ? e : a + static_cast<int64_t>(lane) * step;
-    const int64_t before = pa_units(p, w.s, static_cast<int32_t>(k < e ? k : e));
-    if (head) {  // units of one KV head
-      w.h = y >> 32 || before >> 32
-                ? static_cast<int32_t>(y / before)
-                : static_cast<int32_t>(static_cast<uint32_t>(y) / static_cast<uint32_t>(before));
+    const int32_t k = found ? min(a + lane * step, e) : e;
+    const uint32_t before = pa_units(p, w.s, k);
+    if (!found) {
+      const uint32_t all = before * p.num_kv_heads;
+      if (y >= all) {  // not in this sequence
+        y -= all;
+        at += all;
+        ++w.b;
+        continue;
+      }
+      found = true;
+      w.h = y / before;
       y -= w.h * before;
-      w.u += w.h * before;
+      at += w.h * before;
       continue;
     }
     const int last = 31 - __clz(__ballot_sync(0xffffffffu, k < e && before <= y));
@@ -405,7 +397,7 @@ __device__ __forceinline__ bool pa_plan(const PrefillParams& p, PaBars* bars, Pa
     e = min(e, a + step);
   }
   w.i = a;
-  w.u += start;
+  w.u = at + start;
   w.item(p);
   return true;
 }
@@ -541,10 +533,13 @@ __device__ __forceinline__ void pa_copies(const PrefillParams& p, PaBars* bars,
 // tile's tokens.  Tokens past the item are the next sequence's (or zeros
 // past the batch): rows that are never stored.
 template <int D>
-__device__ __forceinline__ void pa_items(const PrefillParams& p, PaBars* bars, PaWalk<PaSmem<D>::kDual>& w,
-                                         const CUtensorMap* tm_q, uint32_t sq, int64_t units,
-                                         int32_t parts) {
+__device__ __forceinline__ void pa_items(const PrefillParams& p, PaBars* bars,
+                                         const CUtensorMap* tm_q, uint32_t sq,
+                                         const uint32_t* sums) {
   using L = PaSmem<D>;
+  PaWalk<L::kDual> w;
+  uint32_t units, parts;
+  const bool work = pa_plan(p, bars, sums, w, units, parts);
   const int lane = threadIdx.x & 31;
   const uint32_t bytes = static_cast<uint32_t>(p.tok_per_tile * p.group) * D * 2;
   const bool plain = p.q_xor == 0u && p.q_and == 0xffffffffu;
@@ -578,12 +573,9 @@ __device__ __forceinline__ void pa_items(const PrefillParams& p, PaBars* bars, P
     const bool whole = w.j0 == 0 && w.j1 == w.chunks;
     it.flags = (whole ? kPaWhole : 0) | (w.dual(p) ? kPaDual : 0) | (w.j0 == 0 ? kPaHead : 0);
     // the CTA that holds the item's last unit
-    const int64_t x = w.u + kPaItemCost + w.chunks;
-    const uint64_t z = static_cast<uint64_t>(x) * static_cast<uint32_t>(parts) - 1;
     it.job = whole ? -1
-             : z >> 32 || units >> 32
-                 ? static_cast<int32_t>(z / static_cast<uint64_t>(units))
-                 : static_cast<int32_t>(static_cast<uint32_t>(z) / static_cast<uint32_t>(units));
+                   : static_cast<int32_t>(
+                         (static_cast<uint64_t>(w.u + kPaItemCost + w.chunks) * parts - 1) / units);
     return it;
   };
   PaItem it = {};
@@ -592,12 +584,12 @@ __device__ __forceinline__ void pa_items(const PrefillParams& p, PaBars* bars, P
     // the record behind an item goes out before its queries: the copies run
     // ahead into it
     const PaItem cur = it;
-    while (!w.done()) {
+    while (work && !w.done()) {
       if (!first) w.next(p);
       first = false;
       if (w.done() || w.mine) break;
     }
-    if (w.done())
+    if (!work || w.done())
       it.flags = kPaEnd;
     else
       it = record();
@@ -1101,6 +1093,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     mbar_init(smem_addr(&bars->q_raw), 1);
     mbar_init(smem_addr(&bars->ml_full), 4);
     mbar_init(smem_addr(&bars->o_free), 4);
+    bars->bad = 0;
     mbar_fence_init();
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
@@ -1117,19 +1110,19 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   pdl_wait();  // launched as a programmatic dependent: inputs ready below
   pdl_trigger();
 
-  PaWalk<L::kDual> w;
-  int64_t units;
-  int32_t parts;
-  const bool work = pa_plan(p, bars, w, units, parts);
+  // the threads' units, where the ring will be: the copies start behind the
+  // first item's record, which warp 1 writes after it has read them
+  uint32_t* sums = reinterpret_cast<uint32_t*>(pa_smem + L::kOffRing);
+  sums[threadIdx.x] = pa_thread_units(p, bars);
+  fence_proxy_async_smem();
   if (threadIdx.x == 32 * kPaSoftWarp) p.ws_job[blockIdx.x] = make_int4(0, 0, 0, 0);
-  if (!work) {
-    // nothing in this CTA's range
-  } else if (warp < kPaSoftWarp) {
+  __syncthreads();
+  if (warp < kPaSoftWarp) {
     regs_dec<kPaRegsFew>();
     if (warp == 0)
       pa_copies<D>(p, bars, &tm_k, &tm_v, ring);
     else if (warp == 1)
-      pa_items<D>(p, bars, w, &tm_q, sq, units, parts);
+      pa_items<D>(p, bars, &tm_q, sq, sums);
     else
       pa_mma<D>(p, bars, warp - 2, tmem, sq, ring);
   } else {
