@@ -1368,7 +1368,7 @@ size_t prefill_workspace(int64_t P, int32_t head_dim) {
          static_cast<size_t>(P) * sizeof(int4);
 }
 
-template <int D>
+template <int D, bool FP8>
 pa_status launch_prefill(const PrefillParams& prm_in, const void* k_cache, const void* v_cache,
                          void* workspace, size_t workspace_bytes, int32_t num_splits,
                          cudaStream_t stream) {
@@ -1385,10 +1385,10 @@ pa_status launch_prefill(const PrefillParams& prm_in, const void* k_cache, const
     if (!attr_set[dev]) {
       // the register split takes the launch's registers for granted
       cudaFuncAttributes fa;
-      if (cudaFuncGetAttributes(&fa, prefill_kernel<D>) != cudaSuccess) return PA_ERR_CUDA;
-      if (fa.numRegs < kPaRegs) return PA_ERR_UNSUPPORTED;
-      if (cudaFuncSetAttribute(prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               PaSmem<D>::kBytes) != cudaSuccess)
+      if (cudaFuncGetAttributes(&fa, prefill_kernel<D, FP8>) != cudaSuccess) return PA_ERR_CUDA;
+      if (fa.numRegs < PaRegs<FP8>::kLaunch) return PA_ERR_UNSUPPORTED;
+      if (cudaFuncSetAttribute(prefill_kernel<D, FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               PaSmem<D, FP8>::kBytes) != cudaSuccess)
         return PA_ERR_CUDA;
       attr_set[dev] = true;
     }
@@ -1404,11 +1404,16 @@ pa_status launch_prefill(const PrefillParams& prm_in, const void* k_cache, const
   const int32_t box = (p.block_size < kPaChunk ? p.block_size : kPaChunk) / 8;
   CUtensorMap tk, tv, tq;
   if (!encode_queries_4d(&tq, p.q, D, p.num_q_heads, p.num_tokens, p.group, p.tok_per_tile) ||
-      !encode_pool_4d(&tk, k_cache, D, p.groups_total, box) ||
-      !encode_pool_4d(&tv, v_cache, D, p.groups_total, box))
+      !(FP8 ? encode_2d(&tk, CU_TENSOR_MAP_DATA_TYPE_UINT8, k_cache, D, 8ull * p.groups_total, D, D,
+                        8 * box, CU_TENSOR_MAP_SWIZZLE_NONE)
+            : encode_pool_4d(&tk, k_cache, D, p.groups_total, box)) ||
+      !(FP8 ? encode_2d(&tv, CU_TENSOR_MAP_DATA_TYPE_UINT8, v_cache, D, 8ull * p.groups_total, D, D,
+                        8 * box, CU_TENSOR_MAP_SWIZZLE_NONE)
+            : encode_pool_4d(&tv, v_cache, D, p.groups_total, box)))
     return PA_ERR_CUDA;
-  if (launch_pdl(prefill_kernel<D>, dim3(static_cast<unsigned>(P)), dim3(kPaThreads),
-                 PaSmem<D>::kBytes, stream, tk, tv, tq, p) != cudaSuccess)
+  if (launch_pdl(prefill_kernel<D, FP8>, dim3(static_cast<unsigned>(P)),
+                 dim3(PaRegs<FP8>::kThreads), PaSmem<D, FP8>::kBytes, stream, tk, tv, tq,
+                 p) != cudaSuccess)
     return PA_ERR_CUDA;
   return launch_pdl(prefill_merge_kernel<D>, dim3(static_cast<unsigned>(P), kPaItemRows / 32),
                     dim3(256), 0, stream, p) == cudaSuccess
@@ -1444,8 +1449,9 @@ pa_status attention_entry(bool causal, const void* q, const void* k_cache, const
       !aligned4(k_scale) || !aligned4(v_scale))
     return PA_ERR_INVALID_ARG;
   if (kv_dtype == PA_KV_FP8_E4M3 && (!k_scale || !v_scale)) return PA_ERR_INVALID_ARG;
+  // row coordinates of the copies: 8-row groups of a bf16 pool, rows of an FP8 one
   const int64_t groups = static_cast<int64_t>(num_blocks) * num_kv_heads * (block_size / 8);
-  if (groups > INT_MAX - 64) return PA_ERR_UNSUPPORTED;
+  if (groups > (kv_dtype == PA_KV_BF16 ? INT_MAX - 64 : INT_MAX / 8 - 64)) return PA_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(num_tokens) > INT_MAX - 1024) return PA_ERR_UNSUPPORTED;
   // a limit plus a chunk and an item stays within 32 bits
   if (static_cast<int64_t>(max_blocks_per_seq) * block_size > INT_MAX - 1024)
@@ -1461,7 +1467,6 @@ pa_status attention_entry(bool causal, const void* q, const void* k_cache, const
                         max_blocks_per_seq, seq_lens, num_seqs, num_q_heads, num_kv_heads,
                         head_dim, block_size, num_blocks, scale, out, workspace, workspace_bytes,
                         num_splits, stream, nullptr);
-  if (kv_dtype != PA_KV_BF16) return PA_ERR_UNSUPPORTED;
 
   PrefillParams p;
   std::memset(&p, 0, sizeof(p));
@@ -1492,9 +1497,10 @@ pa_status attention_entry(bool causal, const void* q, const void* k_cache, const
   p.q_xor = scale < 0.f && sl > 0.f ? 0x80008000u : 0u;
   p.sl = sl > 0.f ? sl : 1.f;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return head_dim == 128
-             ? launch_prefill<128>(p, k_cache, v_cache, workspace, workspace_bytes, num_splits, s)
-             : launch_prefill<64>(p, k_cache, v_cache, workspace, workspace_bytes, num_splits, s);
+  auto launch = kv_dtype == PA_KV_BF16
+                    ? (head_dim == 128 ? launch_prefill<128, false> : launch_prefill<64, false>)
+                    : (head_dim == 128 ? launch_prefill<128, true> : launch_prefill<64, true>);
+  return launch(p, k_cache, v_cache, workspace, workspace_bytes, num_splits, s);
 }
 
 }  // namespace

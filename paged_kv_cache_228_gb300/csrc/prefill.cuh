@@ -24,6 +24,10 @@
 // An item cut by a range boundary leaves a partial (o unnormalised, m, l)
 // per piece, which prefill_merge_kernel folds; whole items are written
 // directly.  The split depends only on the lengths.
+//
+// FP8 caches: four more warps widen the E4M3 codes to bf16 (exact) between
+// the copies and the MMAs; the per-(block, head) scales never touch the
+// codes: K's multiply the scores, V's the softmax weights, both in fp32.
 #pragma once
 
 #include "pa_device.cuh"
@@ -59,16 +63,25 @@ constexpr int kPaItemRows = kPaRows * kPaTiles;
 constexpr int kPaChunk = 128;          // tokens per chunk
 // Warps: 0 copies K and V, 1 walks the items and loads their queries, 2 and
 // 3 issue the MMAs of tile 0 and 1; 4-7 and 8-11 are the softmax of tile 0
-// and 1.
+// and 1; 12-15 (FP8 only) widen the codes.
 constexpr int kPaWarps = 12;
 constexpr int kPaThreads = 32 * kPaWarps;
 constexpr int kPaSoftWarp = 4;
-// Registers per thread: all warps start with 168 (65536 / 384 in steps of
-// 8); warps 0-3 give up 80 of them to the softmax, whose 128 scores a row
-// stay in registers.  128 * 88 + 256 * 208 = 384 * 168.
-constexpr int kPaRegs = 168, kPaRegsFew = 88, kPaRegsSoft = 208;
-static_assert(128 * kPaRegsFew + 256 * kPaRegsSoft <= kPaThreads * kPaRegs, "register split");
-constexpr int kPaItemCost = 1;         // units charged per item besides its chunks
+constexpr int kPaConvWarp = kPaWarps;
+// Registers per thread.  The launch gives every thread the same (65536 over
+// the threads, in steps of 8); the other warpgroups then give up some to the
+// softmax, whose 128 scores a row stay in registers.
+template <bool FP8>
+struct PaRegs {
+  static constexpr int kThreads = kPaThreads + (FP8 ? 128 : 0);
+  static constexpr int kLaunch = FP8 ? 128 : 168;
+  static constexpr int kFew = FP8 ? 64 : 88;
+  static constexpr int kSoft = FP8 ? 184 : 208;
+  static constexpr int kConv = 80;
+  static_assert(128 * kFew + 256 * kSoft + (FP8 ? 128 * kConv : 0) <= kThreads * kLaunch,
+                "register split");
+};
+constexpr int kPaItemCost = 2;         // units charged per item besides its chunks
 constexpr int kPaTileCols = 256;       // tensor memory per tile: S / P (128), O (D)
 constexpr int kPaSCol = 0;
 constexpr int kPaOCol = 128;
@@ -78,18 +91,27 @@ constexpr int kPaItems = 4;            // item records in flight
 
 constexpr int kPaBarBytes = 1024;
 
-template <int D>
+constexpr int kPaScales = 8;           // chunks whose FP8 scales are kept
+
+template <int D, bool FP8>
 struct PaSmem {
-  static constexpr int kKV = kPaChunk * D * 2;  // K (or V) of a chunk
-  static constexpr int kStages = D == 64 ? 12 : 5;  // one ring: K_j, V_j, K_j+1, ...
+  static constexpr int kKV = kPaChunk * D * 2;  // K (or V) of a chunk, bf16
+  static constexpr int kCodes = kPaChunk * D;   // the same as E4M3
+  // one ring: K_j, V_j, K_j+1, ...; FP8 has a second one of codes before it
+  static constexpr int kStages = FP8 ? (D == 64 ? 8 : 4) : (D == 64 ? 12 : 5);
+  static constexpr int kCodeStages = FP8 ? (D == 64 ? 7 : 2) : 0;
   static constexpr bool kDual = kStages >= 8;
   static constexpr int kQ = kPaRows * D * 2;    // one query tile
   static constexpr int kOffRing = kPaTiles * kQ;
-  static constexpr int kOffMl = kOffRing + kStages * kKV;  // tile 1's (m, l), folded by tile 0
-  static constexpr int kOffBar = kOffMl + kPaRows * 8;
+  static constexpr int kOffCodes = kOffRing + kStages * kKV;
+  static constexpr int kOffMl = kOffCodes + kCodeStages * kCodes;  // tile 1's (m, l), folded by tile 0
+  static constexpr int kOffScale = kOffMl + kPaRows * 8;  // [kPaScales][K, V][16 groups of 8 tokens]
+  static constexpr int kOffBar = kOffScale + (FP8 ? kPaScales * 128 : 0);
   static constexpr int kBytes = kOffBar + kPaBarBytes;
   static constexpr int kGroup = D * 16;         // 8 tokens: D / 64 slabs of 8 x 128 bytes
   static_assert(kStages <= kPaMaxStages && kBytes <= 227 * 1024, "shared memory");
+  // the copies run at most both rings ahead of the softmax
+  static_assert(!FP8 || kStages + kCodeStages <= 2 * kPaScales - 1, "scale ring");
 };
 
 // One item as the walk hands it to the other warps.
@@ -111,6 +133,7 @@ struct PaBars {
   PaItem item[kPaItems];
   uint64_t item_full[kPaItems], item_empty[kPaItems];
   uint64_t full[kPaMaxStages], empty[kPaMaxStages];
+  uint64_t code_full[kPaScales], code_empty[kPaScales], scale_full[kPaScales];  // FP8
   uint64_t q_full[kPaTiles];  // the item's query tile stored
   uint64_t q_raw;             // a query tile before its sign or zero is applied
   uint64_t q_free[kPaTiles];  // the item's last score product of the tile done
@@ -481,12 +504,17 @@ __device__ __forceinline__ void regs_inc() {
 // Warp 0: every chunk's K and V into the ring, one 4D box per block by lane
 // i: 8-token groups of D / 64 slabs of 8 x 128 bytes, so that a single copy
 // carries the block's whole width and successive groups stay one stride
-// apart for the matrix descriptors.
-template <int D>
+// apart for the matrix descriptors.  FP8: plain rows of codes, and each
+// chunk's scales, one per 8 tokens.
+template <int D, bool FP8>
 __device__ __forceinline__ void pa_copies(const PrefillParams& p, PaBars* bars,
                                           const CUtensorMap* tm_k, const CUtensorMap* tm_v,
-                                          uint32_t ring) {
-  using L = PaSmem<D>;
+                                          uint32_t ring, float* scales) {
+  using L = PaSmem<D, FP8>;
+  constexpr uint32_t kS = FP8 ? L::kCodeStages : L::kStages;
+  constexpr uint32_t kBytes = FP8 ? L::kCodes : L::kKV;
+  uint64_t* full = FP8 ? bars->code_full : bars->full;
+  uint64_t* empty = FP8 ? bars->code_empty : bars->empty;
   const int lane = threadIdx.x & 31;
   const int box = p.block_size < kPaChunk ? p.block_size : kPaChunk;
   PaItems items;
@@ -498,32 +526,122 @@ __device__ __forceinline__ void pa_copies(const PrefillParams& p, PaBars* bars,
     const int32_t b = it->b, h = it->h, n = it->n, j0 = it->j0, j1 = it->j1;
     items.put(bars);
     if (j1 <= j0) continue;
-    int32_t e = pa_block_id(p, b, n, j0);
+    // table entries one chunk ahead; FP8: two, and the scales one
+    auto id_of = [&](int32_t j) { return j < j1 ? pa_block_id(p, b, n, j) : -1; };
+    float2 f = make_float2(1.f, 1.f);
+    auto scales_of = [&](int32_t e) {
+      float2 x = make_float2(1.f, 1.f);
+      if (e >= 0 && e < p.num_blocks) {
+        const int64_t i = static_cast<int64_t>(e) * p.num_kv_heads + h;
+        x = make_float2(p.k_scale[i], p.v_scale[i]);
+      }
+      return x;
+    };
+    int32_t e = id_of(j0), e1 = FP8 ? id_of(j0 + 1) : 0;
+    if (FP8) f = scales_of(e);
     for (int32_t j = j0; j < j1 && ok; ++j) {
-      const int32_t en = j + 1 < j1 ? pa_block_id(p, b, n, j + 1) : -1;  // a chunk ahead
+      const int32_t en = id_of(j + (FP8 ? 2 : 1));
+      const float2 fn = FP8 ? scales_of(e1) : f;
       const int32_t grp = pa_block_group(p, h, n, j, e);
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
-        const uint32_t st = slot % L::kStages, use = slot / L::kStages;
-        if (use > 0) ok = pa_wait(smem_addr(&bars->empty[st]), (use - 1) & 1);
+        const uint32_t st = slot % kS, use = slot / kS;
+        if (use > 0) ok = pa_wait(smem_addr(&empty[st]), (use - 1) & 1);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        const uint32_t bar = smem_addr(&bars->full[st]);
-        if (lane == 0) mbar_arrive_expect_tx(bar, L::kKV);
+        if (FP8 && kv == 0) {
+          // group i of 8 tokens lies in block 8 i / box of the chunk
+          const uint32_t c = (slot >> 1) % kPaScales;
+          const int src = (lane & 15) * 8 / box;
+          const float x = __shfl_sync(0xffffffffu, f.x, src), y = __shfl_sync(0xffffffffu, f.y, src);
+          scales[c * 32 + lane] = lane < 16 ? x : y;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_addr(&bars->scale_full[c]));
+        }
+        const uint32_t bar = smem_addr(&full[st]);
+        if (lane == 0) mbar_arrive_expect_tx(bar, kBytes);
         __syncwarp();
-        if (lane < kPaChunk / box)
-          tma_load_4d(ring + st * L::kKV + lane * box * D * 2, kv == 0 ? tm_k : tm_v, 0, 0, 0, grp,
-                      bar);
+        if (lane < kPaChunk / box) {
+          const uint32_t dst = ring + st * kBytes + lane * box * (FP8 ? D : D * 2);
+          if (FP8)
+            tma_load_2d(dst, kv == 0 ? tm_k : tm_v, 0, grp * 8, bar);
+          else
+            tma_load_4d(dst, kv == 0 ? tm_k : tm_v, 0, 0, 0, grp, bar);
+        }
         ++slot;
       }
-      e = en;
+      e = FP8 ? e1 : en;
+      e1 = en;
+      f = fn;
     }
   }
   // No copy may still target shared memory when the CTA exits: on the
   // normal path the MMAs have consumed every one already.
   if (lane == 0)
-    for (uint32_t k = slot < L::kStages ? 0 : slot - L::kStages; k < slot; ++k)
-      pa_wait(smem_addr(&bars->full[k % L::kStages]), (k / L::kStages) & 1, 1u << 16);
+    for (uint32_t k = slot < kS ? 0 : slot - kS; k < slot; ++k)
+      pa_wait(smem_addr(&full[k % kS]), (k / kS) & 1, 1u << 16);
+}
+
+// Warps 12-15 (FP8): codes to bf16, 16 a step: a 16-byte read, and two
+// 16-byte writes into the layout the copies make of a bf16 cache.  E4M3 to
+// f16 to fp32 to bf16, each exact.  A row's two slabs share their banks, so
+// threads of the second slab write their two chunks in the other order.
+template <int D>
+__device__ __forceinline__ void pa_widen(PaBars* bars, uint32_t codes, uint32_t ring) {
+  using L = PaSmem<D, true>;
+  const int t = threadIdx.x - 32 * kPaConvWarp, lane = threadIdx.x & 31;
+  constexpr int kPer = D / 16;  // 16-byte pieces per row of codes
+  PaItems items;
+  uint32_t slot = 0;
+  bool ok = true;
+  while (ok) {
+    const PaItem* it = items.get(bars);
+    if (it == nullptr || (it->flags & kPaEnd)) break;
+    const uint32_t end = slot + 2u * static_cast<uint32_t>(max(it->j1 - it->j0, 0));
+    items.put(bars);
+    for (; slot < end && ok; ++slot) {
+      const uint32_t cs = slot % L::kCodeStages, cu = slot / L::kCodeStages;
+      const uint32_t st = slot % L::kStages, use = slot / L::kStages;
+      ok = pa_wait(smem_addr(&bars->code_full[cs]), cu & 1);
+      if (use > 0) ok = ok && pa_wait(smem_addr(&bars->empty[st]), (use - 1) & 1);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const uint32_t src = codes + cs * L::kCodes, dst = ring + st * L::kKV;
+#pragma unroll 4
+      for (int i = 0; i < kPaChunk * kPer / 128; ++i) {
+        const int idx = t + 128 * i, k = idx / kPer, c = idx % kPer;
+        uint32_t w[4], o[8];
+        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                     : "r"(src + idx * 16)
+                     : "memory");
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t lo, hi;
+          e4m3x4_to_f16x2x2(w[q], lo, hi);
+          const float2 a = unpack_f16x2(lo), b = unpack_f16x2(hi);
+          o[2 * q] = pack_bf16x2(a.x, a.y);
+          o[2 * q + 1] = pack_bf16x2(b.x, b.y);
+        }
+        const int slab = c >> 2, odd = slab & 1;
+        const uint32_t row = dst + (k >> 3) * L::kGroup + slab * 1024 + (k & 7) * 128;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int half = x ^ odd, ch = 2 * (c & 3) + half;
+          asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(row + ((ch ^ (k & 7)) << 4)),
+                       "r"(half ? o[4] : o[0]), "r"(half ? o[5] : o[1]), "r"(half ? o[6] : o[2]),
+                       "r"(half ? o[7] : o[3])
+                       : "memory");
+        }
+      }
+      fence_proxy_async_smem();  // the MMA (async proxy) reads them
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(smem_addr(&bars->full[st]));
+        mbar_arrive(smem_addr(&bars->code_empty[cs]));
+      }
+    }
+  }
 }
 
 // Warp 1: walks the CTA's items, hands each to the other warps, and loads
@@ -532,11 +650,11 @@ __device__ __forceinline__ void pa_copies(const PrefillParams& p, PaBars* bars,
 // P.V product.  One 4D box per 64-column slab: 64 columns x G heads x the
 // tile's tokens.  Tokens past the item are the next sequence's (or zeros
 // past the batch): rows that are never stored.
-template <int D>
+template <int D, bool FP8>
 __device__ __forceinline__ void pa_items(const PrefillParams& p, PaBars* bars,
                                          const CUtensorMap* tm_q, uint32_t sq,
                                          const uint32_t* sums) {
-  using L = PaSmem<D>;
+  using L = PaSmem<D, FP8>;
   PaWalk<L::kDual> w;
   uint32_t units, parts;
   const bool work = pa_plan(p, bars, sums, w, units, parts);
@@ -665,10 +783,10 @@ __device__ __forceinline__ void pa_items(const PrefillParams& p, PaBars* bars,
 // A stage is free once both threads have passed it; for chunks of the other
 // tile (dual items, causal tiles that end earlier) this one only arrives,
 // in ring order.
-template <int D>
+template <int D, bool FP8>
 __device__ __forceinline__ void pa_mma(const PrefillParams& p, PaBars* bars, int t, uint32_t tmem,
                                        uint32_t sq, uint32_t ring) {
-  using L = PaSmem<D>;
+  using L = PaSmem<D, FP8>;
   constexpr uint32_t kIdQK = idesc_bf16(kPaRows, kPaChunk, false, false);
   constexpr uint32_t kIdPV = idesc_bf16(kPaRows, D, false, true);
   const bool leader = (threadIdx.x & 31) == 0;
@@ -838,10 +956,11 @@ __device__ __forceinline__ void pa_store_out(__nv_bfloat16* dst, const float (&o
 // in registers.  The first chunk's m is its own maximum.  The weights are
 // rounded to bf16 (the A operand of the P.V product; half a step is 2^-8 of
 // each) and written over S; l sums them unrounded in fp32.
-template <int D>
+template <int D, bool FP8>
 __device__ __forceinline__ void pa_softmax(const PrefillParams& p, PaBars* bars, int tile,
-                                           uint32_t tmem, uint32_t ring, float2* s_ml) {
-  using L = PaSmem<D>;
+                                           uint32_t tmem, uint32_t ring, float2* s_ml,
+                                           const float* scales) {
+  using L = PaSmem<D, FP8>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int quarter = warp & 3;       // tensor-memory lanes 32 * quarter ...
   const int r = 32 * quarter + lane;  // row within the tile
@@ -868,7 +987,9 @@ __device__ __forceinline__ void pa_softmax(const PrefillParams& p, PaBars* bars,
     float2 la = make_float2(0.f, 0.f);
 #pragma unroll 1
     for (int32_t j = begin; j < end; j += step) {
-      ok = pa_wait(smem_addr(&bars->s_full[tile]), sn++ & 1);
+      const uint32_t chunk = cc + static_cast<uint32_t>(j - j0);
+      ok = !FP8 || pa_wait(smem_addr(&bars->scale_full[chunk % kPaScales]), (chunk / kPaScales) & 1);
+      ok = ok && pa_wait(smem_addr(&bars->s_full[tile]), sn++ & 1);
       if (!__all_sync(0xffffffffu, ok)) {
         ok = false;
         break;
@@ -885,6 +1006,23 @@ __device__ __forceinline__ void pa_softmax(const PrefillParams& p, PaBars* bars,
           for (int c = 0; c < 4; ++c)
             if (__any_sync(0xffffffffu, valid < 32 * c + 32)) pa_mask(u[c], 32 * c, valid);
         }
+        // FP8: K's and V's scales of the chunk, one per 8 columns
+        const float4* sk = reinterpret_cast<const float4*>(scales + (chunk % kPaScales) * 32);
+        if (FP8) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const float4 f = sk[c];
+            const float g[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float2 x = mul2(
+                  make_float2(__uint_as_float(u[c][2 * i]), __uint_as_float(u[c][2 * i + 1])),
+                  make_float2(g[i >> 2], g[i >> 2]));
+              u[c][2 * i] = __float_as_uint(x.x);
+              u[c][2 * i + 1] = __float_as_uint(x.y);
+            }
+          }
+        }
         bool again = j == begin;  // m is this chunk's maximum: no second pass
         if (again) m = pa_row_max(u) * sl;
         float2 sa, sb;
@@ -896,13 +1034,18 @@ __device__ __forceinline__ void pa_softmax(const PrefillParams& p, PaBars* bars,
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             uint32_t pk[16];
+            float g[4];
+            if (FP8) {
+              const float4 f = sk[4 + c];
+              g[0] = f.x, g[1] = f.y, g[2] = f.z, g[3] = f.w;
+            }
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               const float2 x = fma2(
                   make_float2(__uint_as_float(u[c][2 * i]), __uint_as_float(u[c][2 * i + 1])), s2,
                   n2);
               const float2 e = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-              pk[i] = pack_bf16x2(e.x, e.y);
+              pk[i] = FP8 ? pack_bf16x2(e.x * g[i >> 2], e.y * g[i >> 2]) : pack_bf16x2(e.x, e.y);
               if (i & 1)
                 sb = add2(sb, e);
               else
@@ -940,7 +1083,7 @@ __device__ __forceinline__ void pa_softmax(const PrefillParams& p, PaBars* bars,
       // the chunk both do, with the same zeros.
       const int32_t past = n - j * kPaChunk;  // valid tokens of the chunk
       if (past < kPaChunk) {
-        const uint32_t slot = 2 * (cc + static_cast<uint32_t>(j - j0)) + 1;
+        const uint32_t slot = 2 * chunk + 1;
         ok = pa_wait(smem_addr(&bars->full[slot % L::kStages]), (slot / L::kStages) & 1);
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
@@ -1053,12 +1196,12 @@ __device__ __forceinline__ void pa_softmax(const PrefillParams& p, PaBars* bars,
   }
 }
 
-template <int D>
-__global__ void __launch_bounds__(kPaThreads, 1)
+template <int D, bool FP8>
+__global__ void __launch_bounds__(PaRegs<FP8>::kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v,
                    const __grid_constant__ CUtensorMap tm_q, const PrefillParams p) {
-  using L = PaSmem<D>;
+  using L = PaSmem<D, FP8>;
   extern __shared__ __align__(1024) uint8_t pa_smem[];
   const uint32_t base = smem_addr(pa_smem);
   if (base & 1023u) {  // the same for every CTA of the launch
@@ -1074,8 +1217,13 @@ __global__ void __launch_bounds__(kPaThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::kStages; ++i) {
-      mbar_init(smem_addr(&bars->full[i]), 1);
+      mbar_init(smem_addr(&bars->full[i]), FP8 ? 4 : 1);
       mbar_init(smem_addr(&bars->empty[i]), kPaTiles);
+    }
+    for (int i = 0; i < kPaScales && FP8; ++i) {
+      mbar_init(smem_addr(&bars->code_full[i]), 1);
+      mbar_init(smem_addr(&bars->code_empty[i]), 4);
+      mbar_init(smem_addr(&bars->scale_full[i]), 1);
     }
     for (int t = 0; t < kPaTiles; ++t) {
       mbar_init(smem_addr(&bars->q_full[t]), 1);
@@ -1088,7 +1236,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     }
     for (int i = 0; i < kPaItems; ++i) {
       mbar_init(smem_addr(&bars->item_full[i]), 1);
-      mbar_init(smem_addr(&bars->item_empty[i]), 1 + kPaTiles * 5);
+      mbar_init(smem_addr(&bars->item_empty[i]), 1 + kPaTiles * 5 + (FP8 ? 4 : 0));
     }
     mbar_init(smem_addr(&bars->q_raw), 1);
     mbar_init(smem_addr(&bars->ml_full), 4);
@@ -1113,22 +1261,29 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   // the threads' units, where the ring will be: the copies start behind the
   // first item's record, which warp 1 writes after it has read them
   uint32_t* sums = reinterpret_cast<uint32_t*>(pa_smem + L::kOffRing);
-  sums[threadIdx.x] = pa_thread_units(p, bars);
+  if (!FP8 || threadIdx.x < kPaThreads) sums[threadIdx.x] = pa_thread_units(p, bars);
   fence_proxy_async_smem();
   if (threadIdx.x == 32 * kPaSoftWarp) p.ws_job[blockIdx.x] = make_int4(0, 0, 0, 0);
   __syncthreads();
+  using R = PaRegs<FP8>;
+  float* scales = reinterpret_cast<float*>(pa_smem + L::kOffScale);
   if (warp < kPaSoftWarp) {
-    regs_dec<kPaRegsFew>();
+    regs_dec<R::kFew>();
     if (warp == 0)
-      pa_copies<D>(p, bars, &tm_k, &tm_v, ring);
+      pa_copies<D, FP8>(p, bars, &tm_k, &tm_v, FP8 ? base + L::kOffCodes : ring, scales);
     else if (warp == 1)
-      pa_items<D>(p, bars, &tm_q, sq, sums);
+      pa_items<D, FP8>(p, bars, &tm_q, sq, sums);
     else
-      pa_mma<D>(p, bars, warp - 2, tmem, sq, ring);
+      pa_mma<D, FP8>(p, bars, warp - 2, tmem, sq, ring);
+  } else if (!FP8 || warp < kPaConvWarp) {
+    regs_inc<R::kSoft>();
+    pa_softmax<D, FP8>(p, bars, (warp - kPaSoftWarp) >> 2, tmem, ring,
+                       reinterpret_cast<float2*>(pa_smem + L::kOffMl), scales);
   } else {
-    regs_inc<kPaRegsSoft>();
-    pa_softmax<D>(p, bars, (warp - kPaSoftWarp) >> 2, tmem, ring,
-                  reinterpret_cast<float2*>(pa_smem + L::kOffMl));
+    if constexpr (FP8) {
+      regs_dec<R::kConv>();
+      pa_widen<D>(bars, base + L::kOffCodes, ring);
+    }
   }
   tc_fence_before_sync();
   __syncthreads();

@@ -43,7 +43,7 @@ def _check(c, causal, what="", splits=0, scale=None, **kw):
     return out
 
 
-FP8 = [pytest.param(False, id="bf16")]
+FP8 = [pytest.param(False, id="bf16"), pytest.param(True, id="fp8")]
 
 
 @pytest.mark.parametrize("fp8", FP8)
