@@ -565,8 +565,9 @@ pa_status pa_attention_workspace_size(int32_t num_seqs, int32_t num_q_heads,
  * num_kv_heads) and K_b, V_b as in pa_decode:
  *     out[q_start[b] + i][h] = sum_t softmax(scale <q, K_b[t]>)_t V_b[t]
  * with fp32 products and sums; the softmax weights meet V as bf16.  FP8
- * caches read as decode(code) * scale (scales > 0): the codes meet q and
- * the weights exactly, K's scale multiplies the score and V's the weight.
+ * caches read as decode(code) * scale (scales > 0, no NaN codes: the
+ * library's writers store none): the codes meet q and the weights exactly,
+ * K's scale multiplies the score and V's the weight.
  *   q, out       device bf16 [num_tokens][num_q_heads][head_dim]
  *   q_start      device int32 [num_seqs + 1], ascending, within
  *                [0, num_tokens]; NULL: one token per sequence

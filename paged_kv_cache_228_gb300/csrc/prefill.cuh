@@ -148,15 +148,14 @@ struct PaBars {
 };
 static_assert(sizeof(PaBars) <= kPaBarBytes, "barrier block");
 
-// Bounded wait, as mbar_wait; kept to a short loop (not unrolled), since
-// this kernel has some thirty of them and its roles share the SM's
-// instruction cache.
+// Bounded wait, as mbar_wait, but a short loop that leaves the flagging of a
+// timeout to its role's end: this kernel has some thirty waits, and its
+// roles share the SM's instruction cache.
 __device__ __forceinline__ bool pa_wait(uint32_t bar, uint32_t parity,
                                         uint32_t limit = (1u << 22)) {
 #pragma unroll 1
   for (uint32_t i = 0; i < limit; ++i)
     if (mbar_try_wait(bar, parity)) return true;
-  flag_error(PA_DEVERR_TIMEOUT);
   return false;
 }
 
@@ -353,6 +352,12 @@ __device__ __forceinline__ uint32_t pa_warp_sum(uint32_t x) {  // inclusive, ove
   return x;
 }
 
+// floor(units c / parts): the first unit of CTA c.
+__device__ __forceinline__ uint32_t pa_share(uint32_t units, uint32_t parts, uint32_t c) {
+  const uint32_t q = units / parts, rest = units - q * parts;
+  return q * c + rest * c / parts;
+}
+
 // Second part, one warp: this CTA's range and its first item.  `sums`: the
 // threads' units.  Returns false when the CTA has nothing to do.
 template <bool kDual>
@@ -372,9 +377,8 @@ __device__ __forceinline__ bool pa_plan(const PrefillParams& p, PaBars* bars,
   parts = max(1u, min(units / (kPaItemCost + 1), static_cast<uint32_t>(p.num_ctas)));
   const uint32_t c = blockIdx.x;
   if (c >= parts) return false;
-  const uint32_t q = units / parts, rest = units - q * parts;  // floor(units c / parts)
-  w.lo = q * c + rest * c / parts;
-  w.hi = q * (c + 1) + rest * (c + 1) / parts;
+  w.lo = pa_share(units, parts, c);
+  w.hi = pa_share(units, parts, c + 1);
   if (w.lo >= w.hi) return false;
   // the thread whose sequences hold unit lo
   const int li = __ffs(__ballot_sync(0xffffffffu, w.lo < incl)) - 1;
@@ -522,7 +526,11 @@ __device__ __forceinline__ void pa_copies(const PrefillParams& p, PaBars* bars,
   bool ok = true;
   while (ok) {
     const PaItem* it = items.get(bars);
-    if (it == nullptr || (it->flags & kPaEnd)) break;
+    if (it == nullptr) {
+      ok = false;
+      break;
+    }
+    if (it->flags & kPaEnd) break;
     const int32_t b = it->b, h = it->h, n = it->n, j0 = it->j0, j1 = it->j1;
     items.put(bars);
     if (j1 <= j0) continue;
@@ -575,6 +583,7 @@ __device__ __forceinline__ void pa_copies(const PrefillParams& p, PaBars* bars,
       f = fn;
     }
   }
+  if (!ok) flag_error(PA_DEVERR_TIMEOUT);
   // No copy may still target shared memory when the CTA exits: on the
   // normal path the MMAs have consumed every one already.
   if (lane == 0)
@@ -582,10 +591,23 @@ __device__ __forceinline__ void pa_copies(const PrefillParams& p, PaBars* bars,
       pa_wait(smem_addr(&full[k % kS]), (k / kS) & 1, 1u << 16);
 }
 
+// Four E4M3 codes -> two pairs of bf16, exact: a code's exponent and
+// mantissa bits are those of a bf16 value 2^120 smaller (also where they are
+// subnormal), which one multiplication puts right.  Integer instructions: the
+// conversion instructions share the unit of the softmax's exponentials.  The
+// two NaN codes, which no writer of the library stores, come out as +-480.
+__device__ __forceinline__ void e4m3x4_to_bf16x2x2(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  const uint32_t a = __byte_perm(w, 0, 0x1404), b = __byte_perm(w, 0, 0x3424);  // codes << 8
+  const uint32_t x = ((a >> 4) & 0x07f007f0u) | (a & 0x80008000u);
+  const uint32_t y = ((b >> 4) & 0x07f007f0u) | (b & 0x80008000u);
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(lo) : "r"(x), "r"(0x7b807b80u));
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(hi) : "r"(y), "r"(0x7b807b80u));
+}
+
 // Warps 12-15 (FP8): codes to bf16, 16 a step: a 16-byte read, and two
-// 16-byte writes into the layout the copies make of a bf16 cache.  E4M3 to
-// f16 to fp32 to bf16, each exact.  A row's two slabs share their banks, so
-// threads of the second slab write their two chunks in the other order.
+// 16-byte writes into the layout the copies make of a bf16 cache.  A row's
+// two slabs share their banks, so threads of the second slab write their two
+// chunks in the other order.
 template <int D>
 __device__ __forceinline__ void pa_widen(PaBars* bars, uint32_t codes, uint32_t ring) {
   using L = PaSmem<D, true>;
@@ -596,7 +618,11 @@ __device__ __forceinline__ void pa_widen(PaBars* bars, uint32_t codes, uint32_t 
   bool ok = true;
   while (ok) {
     const PaItem* it = items.get(bars);
-    if (it == nullptr || (it->flags & kPaEnd)) break;
+    if (it == nullptr) {
+      ok = false;
+      break;
+    }
+    if (it->flags & kPaEnd) break;
     const uint32_t end = slot + 2u * static_cast<uint32_t>(max(it->j1 - it->j0, 0));
     items.put(bars);
     for (; slot < end && ok; ++slot) {
@@ -617,11 +643,7 @@ __device__ __forceinline__ void pa_widen(PaBars* bars, uint32_t codes, uint32_t 
                      : "memory");
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          uint32_t lo, hi;
-          e4m3x4_to_f16x2x2(w[q], lo, hi);
-          const float2 a = unpack_f16x2(lo), b = unpack_f16x2(hi);
-          o[2 * q] = pack_bf16x2(a.x, a.y);
-          o[2 * q + 1] = pack_bf16x2(b.x, b.y);
+          e4m3x4_to_bf16x2x2(w[q], o[2 * q], o[2 * q + 1]);
         }
         const int slab = c >> 2, odd = slab & 1;
         const uint32_t row = dst + (k >> 3) * L::kGroup + slab * 1024 + (k & 7) * 128;
@@ -642,6 +664,7 @@ __device__ __forceinline__ void pa_widen(PaBars* bars, uint32_t codes, uint32_t 
       }
     }
   }
+  if (!ok) flag_error(PA_DEVERR_TIMEOUT);
 }
 
 // Warp 1: walks the CTA's items, hands each to the other warps, and loads
@@ -690,10 +713,15 @@ __device__ __forceinline__ void pa_items(const PrefillParams& p, PaBars* bars,
     it.end[1] = w.tile_end(p, 1);
     const bool whole = w.j0 == 0 && w.j1 == w.chunks;
     it.flags = (whole ? kPaWhole : 0) | (w.dual(p) ? kPaDual : 0) | (w.j0 == 0 ? kPaHead : 0);
-    // the CTA that holds the item's last unit
-    it.job = whole ? -1
-                   : static_cast<int32_t>(
-                         (static_cast<uint64_t>(w.u + kPaItemCost + w.chunks) * parts - 1) / units);
+    // the CTA that holds the item's last unit: from a lower bound upwards
+    it.job = -1;
+    if (!whole) {
+      const uint32_t x = w.u + kPaItemCost + w.chunks;
+      uint32_t c = (x - 1) / (units / parts + 1);
+#pragma unroll 1
+      while (c < parts - 1 && pa_share(units, parts, c + 1) < x) ++c;
+      it.job = static_cast<int32_t>(c);
+    }
     return it;
   };
   PaItem it = {};
@@ -754,6 +782,7 @@ __device__ __forceinline__ void pa_items(const PrefillParams& p, PaBars* bars,
       if (lane == 0) mbar_arrive(smem_addr(&bars->q_full[t]));
     }
   }
+  if (!ok) flag_error(PA_DEVERR_TIMEOUT);
   // no copy in flight at the end: on the normal path the MMAs have read all.
   // A tile's last load has the parity that its next q_free wait would have.
   if (lane == 0 && plain)
@@ -804,17 +833,13 @@ __device__ __forceinline__ void pa_mma(const PrefillParams& p, PaBars* bars, int
     if (ok) mbar_arrive(smem_addr(&bars->empty[r.stage]));
     r.advance();
   };
-  auto scores = [&](uint32_t st) {
-    const uint32_t kb = ring + st * L::kKV;
-#pragma unroll
-    for (int k = 0; k < D / 16; ++k)
-      umma_bf16(tt + kPaSCol,
-                smem_desc_sw128(qb + (k >> 2) * (kPaRows * 128) + (k & 3) * 32, 16, 1024),
-                smem_desc_sw128(kb + (k >> 2) * 1024 + (k & 3) * 32, 16, L::kGroup), kIdQK, k > 0);
-  };
-  while (true) {
+  while (ok) {
     const PaItem* it = items.get(bars);
-    if (it == nullptr || (it->flags & kPaEnd)) break;
+    if (it == nullptr) {
+      ok = false;
+      break;
+    }
+    if (it->flags & kPaEnd) break;
     if (leader && it->j1 > it->j0) {
       const int32_t j0 = it->j0, j1 = it->j1, end0 = it->end[0], end1 = it->end[1];
       const int32_t end = t == 0 ? end0 : end1;
@@ -828,12 +853,21 @@ __device__ __forceinline__ void pa_mma(const PrefillParams& p, PaBars* bars, int
         pass();
         ++j;
       }
+      auto scores = [&]() {  // of the chunk whose K is the next stage
+        const uint32_t kb = ring + r.stage * L::kKV;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+          umma_bf16(tt + kPaSCol,
+                    smem_desc_sw128(qb + (k >> 2) * (kPaRows * 128) + (k & 3) * 32, 16, 1024),
+                    smem_desc_sw128(kb + (k >> 2) * 1024 + (k & 3) * 32, 16, L::kGroup), kIdQK,
+                    k > 0);
+      };
       if (j < end && ok) {
         ok = full() && pa_wait(smem_addr(&bars->q_full[t]), qph);
         qph ^= 1u;
         if (ok) {
           tc_fence_after_sync();
-          scores(r.stage);
+          scores();
           umma_commit(smem_addr(&bars->s_full[t]));
           umma_commit(smem_addr(&bars->empty[r.stage]));
           if (j + step >= end) umma_commit(smem_addr(&bars->q_free[t]));
@@ -867,7 +901,7 @@ __device__ __forceinline__ void pa_mma(const PrefillParams& p, PaBars* bars, int
           umma_bf16_ta(tt + kPaOCol, tt + kPaSCol + k * 8,
                        smem_desc_sw128(vb + k * 2 * L::kGroup, 1024, L::kGroup), kIdPV,
                        n > 0 || k > 0);
-        if (more) scores(r.stage);
+        if (more) scores();
         if (n < both) mbar_arrive(smem_addr(&bars->turn[1 - t]));
         if (more) {
           umma_commit(smem_addr(&bars->s_full[t]));
@@ -893,6 +927,7 @@ __device__ __forceinline__ void pa_mma(const PrefillParams& p, PaBars* bars, int
     if (!ok) break;
     items.put(bars);
   }
+  if (!ok) flag_error(PA_DEVERR_TIMEOUT);
   // every MMA this thread issued has completed before the tensor memory is
   // released
   if (leader) {
@@ -974,7 +1009,11 @@ __device__ __forceinline__ void pa_softmax(const PrefillParams& p, PaBars* bars,
   bool ok = true;
   while (ok) {
     const PaItem* it = items.get(bars);
-    if (it == nullptr || (it->flags & kPaEnd)) break;
+    if (it == nullptr) {
+      ok = false;
+      break;
+    }
+    if (it->flags & kPaEnd) break;
     const bool dual = L::kDual && (it->flags & kPaDual);
     const int32_t j0 = it->j0, begin = j0 + (dual ? tile : 0), step = dual ? 2 : 1;
     const int32_t end = it->end[tile], n = it->n;
@@ -1023,11 +1062,31 @@ __device__ __forceinline__ void pa_softmax(const PrefillParams& p, PaBars* bars,
             }
           }
         }
-        bool again = j == begin;  // m is this chunk's maximum: no second pass
-        if (again) m = pa_row_max(u) * sl;
+        bool move = j == begin;  // m moves to the maximum of this chunk too
         float2 sa, sb;
 #pragma unroll 1
         while (true) {
+          if (move) {
+            const float mn = fmaxf(m, pa_row_max(u) * sl);
+            if (j > begin) {
+              // O and l scale by alpha.  O holds the products through the
+              // chunk before, all complete (these scores were issued after
+              // them), and this chunk's product waits for this warp's P.
+              const float alpha = mn == -INFINITY ? 1.f : fast_exp2(m - mn);
+              la = mul2(la, make_float2(alpha, alpha));
+#pragma unroll 1
+              for (int c = 0; c < D / 16; ++c) {
+                uint32_t o[16];
+                tmem_ld16(tb + kPaOCol + 16 * c, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                  o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                tmem_st16(tb + kPaOCol + 16 * c, o);
+              }
+            }
+            m = mn;
+          }
           const float neg = m == -INFINITY ? 0.f : -m;  // a row that sees nothing yet
           const float2 s2 = make_float2(sl, sl), n2 = make_float2(neg, neg);
           sa = sb = make_float2(0.f, 0.f);
@@ -1054,26 +1113,9 @@ __device__ __forceinline__ void pa_softmax(const PrefillParams& p, PaBars* bars,
             tmem_st16(tb + kPaSCol + 16 * c, pk);
           }
           const float sum = (sa.x + sa.y) + (sb.x + sb.y);
-          if (again || !__any_sync(0xffffffffu, sum > 256.f || (m == -INFINITY && sum > 0.f)))
+          if (move || !__any_sync(0xffffffffu, sum > 256.f || (m == -INFINITY && sum > 0.f)))
             break;
-          // The running max moves: O and l scale by alpha.  O holds the
-          // products through the chunk before, all complete (these scores
-          // were issued after them), and this chunk's product waits for
-          // this warp's P.
-          again = true;
-          const float mn = fmaxf(m, pa_row_max(u) * sl);
-          const float alpha = mn == -INFINITY ? 1.f : fast_exp2(m - mn);
-          m = mn;
-          la = mul2(la, make_float2(alpha, alpha));
-#pragma unroll 1
-          for (int c = 0; c < D / 16; ++c) {
-            uint32_t o[16];
-            tmem_ld16(tb + kPaOCol + 16 * c, o);
-            tmem_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-            tmem_st16(tb + kPaOCol + 16 * c, o);
-          }
+          move = true;
         }
         la = add2(la, add2(sa, sb));
       }
@@ -1194,6 +1236,7 @@ __device__ __forceinline__ void pa_softmax(const PrefillParams& p, PaBars* bars,
     }
     items.put(bars);
   }
+  if (!ok) flag_error(PA_DEVERR_TIMEOUT);
 }
 
 template <int D, bool FP8>
