@@ -629,22 +629,29 @@ __device__ __forceinline__ void pa_widen(PaBars* bars, uint32_t codes, uint32_t 
       const uint32_t cs = slot % L::kCodeStages, cu = slot / L::kCodeStages;
       const uint32_t st = slot % L::kStages, use = slot / L::kStages;
       ok = pa_wait(smem_addr(&bars->code_full[cs]), cu & 1);
-      if (use > 0) ok = ok && pa_wait(smem_addr(&bars->empty[st]), (use - 1) & 1);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       const uint32_t src = codes + cs * L::kCodes, dst = ring + st * L::kKV;
-#pragma unroll 4
-      for (int i = 0; i < kPaChunk * kPer / 128; ++i) {
-        const int idx = t + 128 * i, k = idx / kPer, c = idx % kPer;
-        uint32_t w[4], o[8];
-        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                     : "r"(src + idx * 16)
-                     : "memory");
+      // all of the thread's codes into registers, and the copies may refill
+      // the stage while they are widened
+      uint32_t w[kPer][4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          e4m3x4_to_bf16x2x2(w[q], o[2 * q], o[2 * q + 1]);
-        }
+      for (int i = 0; i < kPer; ++i)
+        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(w[i][0]), "=r"(w[i][1]), "=r"(w[i][2]), "=r"(w[i][3])
+                     : "r"(src + (t + 128 * i) * 16)
+                     : "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&bars->code_empty[cs]));
+      if (use > 0) ok = pa_wait(smem_addr(&bars->empty[st]), (use - 1) & 1);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int idx = t + 128 * i, k = idx / kPer, c = idx % kPer;
+        uint32_t o[8];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) e4m3x4_to_bf16x2x2(w[i][q], o[2 * q], o[2 * q + 1]);
         const int slab = c >> 2, odd = slab & 1;
         const uint32_t row = dst + (k >> 3) * L::kGroup + slab * 1024 + (k & 7) * 128;
 #pragma unroll
@@ -658,10 +665,7 @@ __device__ __forceinline__ void pa_widen(PaBars* bars, uint32_t codes, uint32_t 
       }
       fence_proxy_async_smem();  // the MMA (async proxy) reads them
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(smem_addr(&bars->full[st]));
-        mbar_arrive(smem_addr(&bars->code_empty[cs]));
-      }
+      if (lane == 0) mbar_arrive(smem_addr(&bars->full[st]));
     }
   }
   if (!ok) flag_error(PA_DEVERR_TIMEOUT);
@@ -985,7 +989,8 @@ __device__ __forceinline__ void pa_store_out(__nv_bfloat16* dst, const float (&o
 // tensor-memory lanes).  A chunk's weights are taken against the running
 // maximum m of the chunks before it, without looking for their own maximum:
 // a row's weights sum to at most 128 unless a score exceeds m, so while no
-// row of the warp sums to more than 2^8, every weight is below 2^8, far from
+// row of the warp sums to more than 2^16, every weight is below 2^16, whose
+// sums and products are as exact as those below 1 and as far from
 // overflow.  Otherwise m moves to the true maximum, O and l are scaled, and
 // the weights are taken again from the scores still
 // in registers.  The first chunk's m is its own maximum.  The weights are
@@ -1113,7 +1118,7 @@ __device__ __forceinline__ void pa_softmax(const PrefillParams& p, PaBars* bars,
             tmem_st16(tb + kPaSCol + 16 * c, pk);
           }
           const float sum = (sa.x + sa.y) + (sb.x + sb.y);
-          if (move || !__any_sync(0xffffffffu, sum > 256.f || (m == -INFINITY && sum > 0.f)))
+          if (move || !__any_sync(0xffffffffu, sum > 65536.f || (m == -INFINITY && sum > 0.f)))
             break;
           move = true;
         }
