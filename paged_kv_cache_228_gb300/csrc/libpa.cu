@@ -1415,8 +1415,11 @@ pa_status launch_prefill(const PrefillParams& prm_in, const void* k_cache, const
                  dim3(PaRegs<FP8>::kThreads), PaSmem<D, FP8>::kBytes, stream, tk, tv, tq,
                  p) != cudaSuccess)
     return PA_ERR_CUDA;
+  // an item of one chunk is never cut: nothing to fold where the tables hold
+  // no more than that
+  if (static_cast<int64_t>(p.max_blocks) * p.block_size <= kPaChunk) return PA_OK;
   return launch_pdl(prefill_merge_kernel<D>, dim3(static_cast<unsigned>(P), kPaItemRows / 32),
-                    dim3(256), 0, stream, p) == cudaSuccess
+                    dim3(2 * D), 0, stream, p) == cudaSuccess
              ? PA_OK
              : PA_ERR_CUDA;
 }

@@ -67,6 +67,7 @@ constexpr int kPaChunk = 128;          // tokens per chunk
 constexpr int kPaWarps = 12;
 constexpr int kPaThreads = 32 * kPaWarps;
 constexpr int kPaSoftWarp = 4;
+constexpr int kPaSoftWarps = 8;
 constexpr int kPaConvWarp = kPaWarps;
 // Registers per thread.  The launch gives every thread the same (65536 over
 // the threads, in steps of 8); the other warpgroups then give up some to the
@@ -98,14 +99,18 @@ struct PaSmem {
   static constexpr int kKV = kPaChunk * D * 2;  // K (or V) of a chunk, bf16
   static constexpr int kCodes = kPaChunk * D;   // the same as E4M3
   // one ring: K_j, V_j, K_j+1, ...; FP8 has a second one of codes before it
-  static constexpr int kStages = FP8 ? (D == 64 ? 8 : 4) : (D == 64 ? 12 : 5);
-  static constexpr int kCodeStages = FP8 ? (D == 64 ? 7 : 2) : 0;
+  static constexpr int kStages = FP8 ? (D == 64 ? 8 : 4) : (D == 64 ? 10 : 4);
+  static constexpr int kCodeStages = FP8 ? (D == 64 ? 4 : 2) : 0;
+  // 4 KB per softmax warp to turn rows into whole lines on their way out; not
+  // where the codes' ring leaves no room
+  static constexpr bool kStageOut = !FP8 || D == 64;
   static constexpr bool kDual = kStages >= 8;
   static constexpr int kQ = kPaRows * D * 2;    // one query tile
   static constexpr int kOffRing = kPaTiles * kQ;
   static constexpr int kOffCodes = kOffRing + kStages * kKV;
   static constexpr int kOffMl = kOffCodes + kCodeStages * kCodes;  // tile 1's (m, l), folded by tile 0
-  static constexpr int kOffScale = kOffMl + kPaRows * 8;  // [kPaScales][K, V][16 groups of 8 tokens]
+  static constexpr int kOffOut = kOffMl + kPaRows * 8;
+  static constexpr int kOffScale = kOffOut + (kStageOut ? kPaSoftWarps * 4096 : 0);  // [kPaScales][K, V][16 groups of 8 tokens]
   static constexpr int kOffBar = kOffScale + (FP8 ? kPaScales * 128 : 0);
   static constexpr int kBytes = kOffBar + kPaBarBytes;
   static constexpr int kGroup = D * 16;         // 8 tokens: D / 64 slabs of 8 x 128 bytes
@@ -962,14 +967,11 @@ __device__ __forceinline__ float pa_row_max(const uint32_t (&u)[4][32]) {
   return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
 
-// 32 columns of an output row as bf16: two stores of a whole 32-byte sector
-// each (a row is its own thread's, so narrower stores would send every
-// sector twice), or 16-byte stores where out is only 16-byte aligned.
-__device__ __forceinline__ void pa_store_out(__nv_bfloat16* dst, const float (&o)[32],
+// 32 columns of an output row as bf16, from the row's own thread: two stores
+// of a whole 32-byte sector each, or 16-byte stores where out is only
+// 16-byte aligned.
+__device__ __forceinline__ void pa_store_row(__nv_bfloat16* dst, const uint32_t (&x)[16],
                                              bool wide) {
-  uint32_t x[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) x[i] = pack_bf16x2(o[2 * i], o[2 * i + 1]);
   if (wide) {
 #pragma unroll
     for (int i = 0; i < 2; ++i)
@@ -999,7 +1001,7 @@ __device__ __forceinline__ void pa_store_out(__nv_bfloat16* dst, const float (&o
 template <int D, bool FP8>
 __device__ __forceinline__ void pa_softmax(const PrefillParams& p, PaBars* bars, int tile,
                                            uint32_t tmem, uint32_t ring, float2* s_ml,
-                                           const float* scales) {
+                                           const float* scales, uint32_t stage) {
   using L = PaSmem<D, FP8>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int quarter = warp & 3;       // tensor-memory lanes 32 * quarter ...
@@ -1192,9 +1194,21 @@ __device__ __forceinline__ void pa_softmax(const PrefillParams& p, PaBars* bars,
       // slot 0 (it is then the CTA's first item)
       const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (it->flags & kPaHead ? 1 : 0);
       float4* po = reinterpret_cast<float4*>(p.ws_o) + slot * (D / 4) * kPaItemRows + row;
-      __nv_bfloat16* po16 =
-          p.out + (static_cast<int64_t>(it->row + tk) * p.num_q_heads +
-                   it->h * p.group + (r - rt * p.group)) * D;
+      // out row of row x of the tile, -1 where it has none
+      const int32_t nt = it->nt, tk0 = dual ? 0 : tile * p.tok_per_tile;
+      auto out_row = [&](int32_t x) -> int32_t {
+        const int32_t xt = static_cast<int32_t>(pa_div(p, static_cast<uint32_t>(x)));
+        return xt < p.tok_per_tile && xt + tk0 < nt
+                   ? (xt + tk0) * p.num_q_heads + (x - xt * p.group)
+                   : -1;
+      };
+      int32_t mine[8];  // of the rows that this lane writes
+      if (L::kStageOut) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) mine[i] = out_row(32 * quarter + 4 * i + (lane >> 3));
+      }
+      __nv_bfloat16* out0 =
+          p.out + (static_cast<int64_t>(it->row) * p.num_q_heads + it->h * p.group) * D;
       if (!whole && has) p.ws_ml[slot * kPaItemRows + row] = make_float2(m, l);
       if (whole) {
         const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -1221,15 +1235,48 @@ __device__ __forceinline__ void pa_softmax(const PrefillParams& p, PaBars* bars,
 #pragma unroll
           for (int i = 0; i < 32; ++i) x[i] = 0.f;
         }
-        if (!has) continue;
-        if (whole) {
-          pa_store_out(po16 + 32 * c, x, wide);
-        } else {
+        if (!whole) {
+          if (has) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            po[(8 * c + i) * kPaItemRows] =
-                make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+            for (int i = 0; i < 8; ++i)
+              po[(8 * c + i) * kPaItemRows] =
+                  make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+          }
+          continue;
         }
+        uint32_t y[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) y[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+        if (!L::kStageOut) {
+          const int32_t k = out_row(r);
+          if (has) pa_store_row(out0 + static_cast<int64_t>(k) * D + 32 * c, y, wide);
+          continue;
+        }
+        // Stored from its own thread, every row would touch its own lines: 32
+        // of them per instruction, some 800 cycles for 32 columns of both
+        // tiles.  64 columns at a time go through the warp's 4 KB of shared
+        // memory (16-byte chunk i of row x at i ^ (x % 8)); then eight lanes
+        // write 128 contiguous bytes of a row.
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(
+                           stage + lane * 128 + (((4 * (c & 1) + i) ^ (lane & 7)) << 4)),
+                       "r"(y[4 * i]), "r"(y[4 * i + 1]), "r"(y[4 * i + 2]), "r"(y[4 * i + 3])
+                       : "memory");
+        if ((c & 1) == 0) continue;
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int x4 = 4 * i + (lane >> 3);
+          uint4 z;
+          asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                       : "=r"(z.x), "=r"(z.y), "=r"(z.z), "=r"(z.w)
+                       : "r"(stage + x4 * 128 + (((lane & 7) ^ (x4 & 7)) << 4))
+                       : "memory");
+          if (mine[i] >= 0)
+            reinterpret_cast<uint4*>(out0 + static_cast<int64_t>(mine[i]) * D + 64 * (c >> 1))[lane & 7] = z;
+        }
+        __syncwarp();
       }
       if (!whole && (it->flags & kPaHead) && threadIdx.x == 32 * kPaSoftWarp)
         p.ws_job[blockIdx.x] = make_int4(it->job, it->row, it->h, it->nt);
@@ -1326,7 +1373,8 @@ __global__ void __launch_bounds__(PaRegs<FP8>::kThreads, 1)
   } else if (!FP8 || warp < kPaConvWarp) {
     regs_inc<R::kSoft>();
     pa_softmax<D, FP8>(p, bars, (warp - kPaSoftWarp) >> 2, tmem, ring,
-                       reinterpret_cast<float2*>(pa_smem + L::kOffMl), scales);
+                       reinterpret_cast<float2*>(pa_smem + L::kOffMl), scales,
+                       base + L::kOffOut + (warp - kPaSoftWarp) * 4096);
   } else {
     if constexpr (FP8) {
       regs_dec<R::kConv>();
@@ -1342,12 +1390,14 @@ __global__ void __launch_bounds__(PaRegs<FP8>::kThreads, 1)
 }
 
 // Folds the pieces of each item that a range boundary cut: M = max m_i,
-// out = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i (0 without any key).
-// Block (c, part): 32 rows of the item whose head piece CTA c holds; lane =
-// row, so every load of the piece's [D / 4][256] float4 is coalesced; warp w
-// takes 8 columns a step.
+// out = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i (0 without any key), as a
+// running sum over the pieces.  Block (c, part): 32 rows of the item whose
+// head piece CTA c holds; lane = row, so every load of a piece's [D / 4][256]
+// float4 is coalesced; warp w has columns 16 w ..  Bound by latency (few
+// pieces, read from L2): the loads of two pieces, the usual number, are all
+// in flight together.
 template <int D>
-__global__ void __launch_bounds__(256) prefill_merge_kernel(const PrefillParams p) {
+__global__ void __launch_bounds__(2 * D) prefill_merge_kernel(const PrefillParams p) {
   pdl_wait();
   pdl_trigger();
   const int32_t c = blockIdx.x;
@@ -1356,41 +1406,67 @@ __global__ void __launch_bounds__(256) prefill_merge_kernel(const PrefillParams 
   const int32_t r = row & (kPaRows - 1), rt = static_cast<int32_t>(pa_div(p, r));
   const int32_t tk = rt + (row >= kPaRows ? p.tok_per_tile : 0);
   if (rt >= p.tok_per_tile || tk >= job.w || job.x >= p.num_ctas) return;
-  auto slot = [&](int32_t i) -> int64_t { return 2 * static_cast<int64_t>(i) + (i == c ? 1 : 0); };
-  float M = -INFINITY;
-  for (int32_t i = c; i <= job.x; ++i) M = fmaxf(M, p.ws_ml[slot(i) * kPaItemRows + row].x);
+  constexpr int kBatch = 2;
+  float M = -INFINITY, l = 0.f;
+  float acc[16];
+#pragma unroll
+  for (int k = 0; k < 16; ++k) acc[k] = 0.f;
+  for (int32_t i0 = c; i0 <= job.x; i0 += kBatch) {
+    float2 ml[kBatch];
+    float4 x[kBatch][4];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      ml[i] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[i][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i0 + i <= job.x) {
+        const int64_t s = 2 * static_cast<int64_t>(i0 + i) + (i0 + i == c ? 1 : 0);
+        ml[i] = p.ws_ml[s * kPaItemRows + row];
+        const float4* po = reinterpret_cast<const float4*>(p.ws_o) +
+                           (s * (D / 4) + 4 * warp) * kPaItemRows + row;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[i][k] = po[k * kPaItemRows];
+      }
+    }
+    float mn = M;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) mn = fmaxf(mn, ml[i].x);
+    if (mn == -INFINITY) {  // no piece so far has a key for the row (or all its scores are NaN)
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) l += ml[i].y;
+      continue;
+    }
+    const float w0 = fast_exp2(M - mn);
+    M = mn;
+    l *= w0;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) acc[k] *= w0;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      // a piece that the row sees nothing of weighs 0
+      const float wgt = ml[i].x == -INFINITY ? 0.f : fast_exp2(ml[i].x - mn);
+      l = fmaf(wgt, ml[i].y, l);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        acc[4 * k] = fmaf(wgt, x[i][k].x, acc[4 * k]);
+        acc[4 * k + 1] = fmaf(wgt, x[i][k].y, acc[4 * k + 1]);
+        acc[4 * k + 2] = fmaf(wgt, x[i][k].z, acc[4 * k + 2]);
+        acc[4 * k + 3] = fmaf(wgt, x[i][k].w, acc[4 * k + 3]);
+      }
+    }
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
   const int64_t orow = static_cast<int64_t>(job.y + tk) * p.num_q_heads + job.z * p.group +
                        (r - rt * p.group);
+  uint4* dst = reinterpret_cast<uint4*>(p.out + orow * D + 16 * warp);
 #pragma unroll
-  for (int cc = 0; cc < D / 64; ++cc) {
-    const int col = warp + 8 * cc;  // 8 columns each
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
-    float l = 0.f;
-    for (int32_t i = c; i <= job.x; ++i) {
-      const int64_t s = slot(i);
-      const float2 ml = p.ws_ml[s * kPaItemRows + row];
-      const float4* po = reinterpret_cast<const float4*>(p.ws_o) +
-                         (s * (D / 4) + 2 * col) * kPaItemRows + row;
-      const float4 x = po[0], y = po[kPaItemRows];
-      if (ml.x == -INFINITY) continue;  // a piece the row sees nothing of
-      const float wgt = fast_exp2(ml.x - M);
-      l = fmaf(wgt, ml.y, l);
-      a.x = fmaf(wgt, x.x, a.x);
-      a.y = fmaf(wgt, x.y, a.y);
-      a.z = fmaf(wgt, x.z, a.z);
-      a.w = fmaf(wgt, x.w, a.w);
-      b.x = fmaf(wgt, y.x, b.x);
-      b.y = fmaf(wgt, y.y, b.y);
-      b.z = fmaf(wgt, y.z, b.z);
-      b.w = fmaf(wgt, y.w, b.w);
-    }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+  for (int h = 0; h < 2; ++h) {
     uint4 o;
-    o.x = pack_bf16x2(a.x * inv, a.y * inv);
-    o.y = pack_bf16x2(a.z * inv, a.w * inv);
-    o.z = pack_bf16x2(b.x * inv, b.y * inv);
-    o.w = pack_bf16x2(b.z * inv, b.w * inv);
-    reinterpret_cast<uint4*>(p.out + orow * D)[col] = o;
+    o.x = pack_bf16x2(acc[8 * h] * inv, acc[8 * h + 1] * inv);
+    o.y = pack_bf16x2(acc[8 * h + 2] * inv, acc[8 * h + 3] * inv);
+    o.z = pack_bf16x2(acc[8 * h + 4] * inv, acc[8 * h + 5] * inv);
+    o.w = pack_bf16x2(acc[8 * h + 6] * inv, acc[8 * h + 7] * inv);
+    dst[h] = o;
   }
 }
 
