@@ -475,10 +475,11 @@ __device__ __forceinline__ int32_t pa_block_group(const PrefillParams& p, int32_
 // A consumer's place in the item records.
 struct PaItems {
   uint32_t k = 0;
-  // the next record; NULL after a failed wait
-  __device__ __forceinline__ const PaItem* get(PaBars* bars) {
-    const bool ok = pa_wait(smem_addr(&bars->item_full[k % kPaItems]), (k / kPaItems) & 1);
-    return __all_sync(0xffffffffu, ok) ? &bars->item[k % kPaItems] : nullptr;
+  // the record `ahead` of this one; NULL after a failed wait
+  __device__ __forceinline__ const PaItem* get(PaBars* bars, uint32_t ahead = 0) {
+    const uint32_t i = k + ahead;
+    const bool ok = pa_wait(smem_addr(&bars->item_full[i % kPaItems]), (i / kPaItems) & 1);
+    return __all_sync(0xffffffffu, ok) ? &bars->item[i % kPaItems] : nullptr;
   }
   // the warp has read it
   __device__ __forceinline__ void put(PaBars* bars) {
@@ -954,17 +955,15 @@ __device__ __forceinline__ void pa_mask(uint32_t (&u)[32], int32_t c0, int32_t v
   for (int i = 0; i < 32; ++i) u[i] = c0 + i < valid ? u[i] : 0xff800000u;
 }
 
-// The largest of a thread's 128 scores: three-input maxima in four chains.
-__device__ __forceinline__ float pa_row_max(const uint32_t (&u)[4][32]) {
-  float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+// The largest of 32 scores: three-input maxima in two chains.
+__device__ __forceinline__ float pa_max32(const uint32_t (&u)[32]) {
+  float m[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-  for (int c = 0; c < 4; ++c)
+  for (int i = 0; i < 32; i += 4)
 #pragma unroll
-    for (int i = 0; i < 32; i += 8)
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        m[k] = fmax3(m[k], __uint_as_float(u[c][i + 2 * k]), __uint_as_float(u[c][i + 2 * k + 1]));
-  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+    for (int k = 0; k < 2; ++k)
+      m[k] = fmax3(m[k], __uint_as_float(u[i + 2 * k]), __uint_as_float(u[i + 2 * k + 1]));
+  return fmaxf(m[0], m[1]);
 }
 
 // 32 columns of an output row as bf16, from the row's own thread: two stores
@@ -989,15 +988,15 @@ __device__ __forceinline__ void pa_store_row(__nv_bfloat16* dst, const uint32_t 
 
 // Warps 4-11: four per tile, one row per thread (the warp's quarter of the
 // tensor-memory lanes).  A chunk's weights are taken against the running
-// maximum m of the chunks before it, without looking for their own maximum:
-// a row's weights sum to at most 128 unless a score exceeds m, so while no
-// row of the warp sums to more than 2^16, every weight is below 2^16, whose
-// sums and products are as exact as those below 1 and as far from
-// overflow.  Otherwise m moves to the true maximum, O and l are scaled, and
-// the weights are taken again from the scores still
-// in registers.  The first chunk's m is its own maximum.  The weights are
-// rounded to bf16 (the A operand of the P.V product; half a step is 2^-8 of
-// each) and written over S; l sums them unrounded in fp32.
+// maximum m, which need not be the true one: m starts as the maximum of the
+// first chunk's first 32 scores, and while no row of the warp has weights
+// that sum to more than 2^16, every weight is below 2^16, whose sums and
+// products are as exact as those below 1 and far from overflow.  Otherwise
+// (or when a row sees its first key) m moves to the true maximum, O and l
+// are scaled, and the weights are taken again from the scores still in
+// registers.  The weights are rounded to bf16 (the A operand of the P.V
+// product; half a step is 2^-8 of each) and written over S; l sums them
+// unrounded in fp32.
 template <int D, bool FP8>
 __device__ __forceinline__ void pa_softmax(const PrefillParams& p, PaBars* bars, int tile,
                                            uint32_t tmem, uint32_t ring, float2* s_ml,
@@ -1014,8 +1013,8 @@ __device__ __forceinline__ void pa_softmax(const PrefillParams& p, PaBars* bars,
   PaItems items;
   uint32_t sn = 0, on = 0, cc = 0, dn = 0;  // S tiles, items, chunks of the CTA, dual items
   bool ok = true;
-  while (ok) {
-    const PaItem* it = items.get(bars);
+  const PaItem* it = items.get(bars);
+  while (true) {
     if (it == nullptr) {
       ok = false;
       break;
@@ -1069,12 +1068,14 @@ __device__ __forceinline__ void pa_softmax(const PrefillParams& p, PaBars* bars,
             }
           }
         }
-        bool move = j == begin;  // m moves to the maximum of this chunk too
+        if (j == begin) m = pa_max32(u[0]) * sl;
+        bool move = false;  // m moves to the maximum of this chunk too
         float2 sa, sb;
 #pragma unroll 1
         while (true) {
           if (move) {
-            const float mn = fmaxf(m, pa_row_max(u) * sl);
+            const float mn = fmaxf(m, fmaxf(fmaxf(pa_max32(u[0]), pa_max32(u[1])),
+                                            fmaxf(pa_max32(u[2]), pa_max32(u[3]))) * sl);
             if (j > begin) {
               // O and l scale by alpha.  O holds the products through the
               // chunk before, all complete (these scores were issued after
@@ -1156,6 +1157,7 @@ __device__ __forceinline__ void pa_softmax(const PrefillParams& p, PaBars* bars,
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_addr(&bars->p_full[tile]));
     }
+    const PaItem* next = ok ? items.get(bars, 1) : nullptr;  // there already as a rule
     if (end > begin && ok) {
       ok = pa_wait(smem_addr(&bars->o_last[tile]), on++ & 1);
       ok = __all_sync(0xffffffffu, ok);
@@ -1174,6 +1176,7 @@ __device__ __forceinline__ void pa_softmax(const PrefillParams& p, PaBars* bars,
         ok = pa_wait(smem_addr(&bars->o_free), dn++ & 1);
         ok = __all_sync(0xffffffffu, ok);
         items.put(bars);
+        it = ok ? next : nullptr;
         continue;
       }
       ok = pa_wait(smem_addr(&bars->ml_full), dn++ & 1);
@@ -1219,19 +1222,23 @@ __device__ __forceinline__ void pa_softmax(const PrefillParams& p, PaBars* bars,
       for (int c = 0; c < D / 32; ++c) {
         uint32_t o[32];
         float x[32];
-        if (end > begin) {
+        if (__any_sync(0xffffffffu, l != 0.f)) {
           tmem_ld32(tb + kPaOCol + 32 * c, o);
           tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) x[i] = l == 0.f ? 0.f : __uint_as_float(o[i]) * w0;
+          for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(o[i]) * w0;
           if (dual) {
             tmem_ld32(tb + kPaTileCols + kPaOCol + 32 * c, o);
             tmem_wait_ld();
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-              x[i] = l == 0.f ? 0.f : fmaf(__uint_as_float(o[i]), w1, x[i]);
+              x[i] = fmaf(__uint_as_float(o[i]), w1, x[i]);
           }
         } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) x[i] = 0.f;
+        }
+        if (l == 0.f) {  // a row that saw nothing: zeros, whatever V holds
 #pragma unroll
           for (int i = 0; i < 32; ++i) x[i] = 0.f;
         }
@@ -1287,6 +1294,7 @@ __device__ __forceinline__ void pa_softmax(const PrefillParams& p, PaBars* bars,
       if (lane == 0) mbar_arrive(smem_addr(&bars->o_free));
     }
     items.put(bars);
+    it = next;
   }
   if (!ok) flag_error(PA_DEVERR_TIMEOUT);
 }
