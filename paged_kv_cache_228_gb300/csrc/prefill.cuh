@@ -27,7 +27,9 @@
 //
 // FP8 caches: four more warps widen the E4M3 codes to bf16 (exact) between
 // the copies and the MMAs; the per-(block, head) scales never touch the
-// codes: K's multiply the scores, V's the softmax weights, both in fp32.
+// codes: K's multiply the scores, V's the softmax weights, both in fp32 and
+// both inside the exponent's one multiply-add per score,
+//     v 2^(s k sl - m) = 2^(s (k sl) + (log2 v - m)).
 #pragma once
 
 #include "pa_device.cuh"
@@ -91,8 +93,10 @@ constexpr int kPaMaxStages = 12;
 constexpr int kPaItems = 4;            // item records in flight
 
 constexpr int kPaBarBytes = 1024;
+constexpr int kPaMaxCodeStages = 8;
+// per chunk and 8 tokens: k, log2 v, 1 / v
+constexpr int kPaScaleFloats = 48;
 
-constexpr int kPaScales = 8;           // chunks whose FP8 scales are kept
 
 template <int D, bool FP8>
 struct PaSmem {
@@ -100,7 +104,7 @@ struct PaSmem {
   static constexpr int kCodes = kPaChunk * D;   // the same as E4M3
   // one ring: K_j, V_j, K_j+1, ...; FP8 has a second one of codes before it
   static constexpr int kStages = FP8 ? (D == 64 ? 8 : 4) : (D == 64 ? 10 : 4);
-  static constexpr int kCodeStages = FP8 ? (D == 64 ? 4 : 2) : 0;
+  static constexpr int kCodeStages = FP8 ? (D == 64 ? 3 : 2) : 0;
   // 4 KB per softmax warp to turn rows into whole lines on their way out; not
   // where the codes' ring leaves no room
   static constexpr bool kStageOut = !FP8 || D == 64;
@@ -110,13 +114,14 @@ struct PaSmem {
   static constexpr int kOffCodes = kOffRing + kStages * kKV;
   static constexpr int kOffMl = kOffCodes + kCodeStages * kCodes;  // tile 1's (m, l), folded by tile 0
   static constexpr int kOffOut = kOffMl + kPaRows * 8;
-  static constexpr int kOffScale = kOffOut + (kStageOut ? kPaSoftWarps * 4096 : 0);  // [kPaScales][K, V][16 groups of 8 tokens]
-  static constexpr int kOffBar = kOffScale + (FP8 ? kPaScales * 128 : 0);
+  static constexpr int kScales = D == 64 ? 8 : 4;  // chunks whose FP8 scales are kept
+  static constexpr int kOffScale = kOffOut + (kStageOut ? kPaSoftWarps * 4096 : 0);  
+  static constexpr int kOffBar = kOffScale + (FP8 ? kScales * kPaScaleFloats * 4 : 0);
   static constexpr int kBytes = kOffBar + kPaBarBytes;
   static constexpr int kGroup = D * 16;         // 8 tokens: D / 64 slabs of 8 x 128 bytes
   static_assert(kStages <= kPaMaxStages && kBytes <= 227 * 1024, "shared memory");
   // the copies run at most both rings ahead of the softmax
-  static_assert(!FP8 || kStages + kCodeStages <= 2 * kPaScales - 1, "scale ring");
+  static_assert(!FP8 || kStages + kCodeStages <= 2 * kScales - 1, "scale ring");
 };
 
 // One item as the walk hands it to the other warps.
@@ -138,7 +143,8 @@ struct PaBars {
   PaItem item[kPaItems];
   uint64_t item_full[kPaItems], item_empty[kPaItems];
   uint64_t full[kPaMaxStages], empty[kPaMaxStages];
-  uint64_t code_full[kPaScales], code_empty[kPaScales], scale_full[kPaScales];  // FP8
+  uint64_t code_full[kPaMaxCodeStages], code_empty[kPaMaxCodeStages];  // FP8
+  uint64_t scale_full[kPaMaxCodeStages];
   uint64_t q_full[kPaTiles];  // the item's query tile stored
   uint64_t q_raw;             // a query tile before its sign or zero is applied
   uint64_t q_free[kPaTiles];  // the item's last score product of the tile done
@@ -547,7 +553,7 @@ __device__ __forceinline__ void pa_copies(const PrefillParams& p, PaBars* bars,
       float2 x = make_float2(1.f, 1.f);
       if (e >= 0 && e < p.num_blocks) {
         const int64_t i = static_cast<int64_t>(e) * p.num_kv_heads + h;
-        x = make_float2(p.k_scale[i], p.v_scale[i]);
+        x = make_float2(p.k_scale[i], fmaxf(p.v_scale[i], 0x1p-120f));  // 1 / v stays finite
       }
       return x;
     };
@@ -565,10 +571,12 @@ __device__ __forceinline__ void pa_copies(const PrefillParams& p, PaBars* bars,
         if (!ok) break;
         if (FP8 && kv == 0) {
           // group i of 8 tokens lies in block 8 i / box of the chunk
-          const uint32_t c = (slot >> 1) % kPaScales;
+          const uint32_t c = (slot >> 1) % L::kScales;
           const int src = (lane & 15) * 8 / box;
           const float x = __shfl_sync(0xffffffffu, f.x, src), y = __shfl_sync(0xffffffffu, f.y, src);
-          scales[c * 32 + lane] = lane < 16 ? x : y;
+          float* to = scales + c * kPaScaleFloats;
+          to[lane] = lane < 16 ? x : log2f(y);
+          if (lane < 16) to[32 + lane] = 1.f / y;
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_addr(&bars->scale_full[c]));
         }
@@ -966,6 +974,21 @@ __device__ __forceinline__ float pa_max32(const uint32_t (&u)[32]) {
   return fmaxf(m[0], m[1]);
 }
 
+// The same with a factor for each 8 of them.
+__device__ __forceinline__ float pa_max32(const uint32_t (&u)[32], float4 f) {
+  const float g[4] = {f.x, f.y, f.z, f.w};
+  float m = -INFINITY;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    float x = -INFINITY;
+#pragma unroll
+    for (int i = 8 * q; i < 8 * q + 8; i += 2)
+      x = fmax3(x, __uint_as_float(u[i]), __uint_as_float(u[i + 1]));
+    m = fmaxf(m, x * g[q]);
+  }
+  return m;
+}
+
 // 32 columns of an output row as bf16, from the row's own thread: two stores
 // of a whole 32-byte sector each, or 16-byte stores where out is only
 // 16-byte aligned.
@@ -1033,7 +1056,7 @@ __device__ __forceinline__ void pa_softmax(const PrefillParams& p, PaBars* bars,
 #pragma unroll 1
     for (int32_t j = begin; j < end; j += step) {
       const uint32_t chunk = cc + static_cast<uint32_t>(j - j0);
-      ok = !FP8 || pa_wait(smem_addr(&bars->scale_full[chunk % kPaScales]), (chunk / kPaScales) & 1);
+      ok = !FP8 || pa_wait(smem_addr(&bars->scale_full[chunk % L::kScales]), (chunk / L::kScales) & 1);
       ok = ok && pa_wait(smem_addr(&bars->s_full[tile]), sn++ & 1);
       if (!__all_sync(0xffffffffu, ok)) {
         ok = false;
@@ -1051,31 +1074,20 @@ __device__ __forceinline__ void pa_softmax(const PrefillParams& p, PaBars* bars,
           for (int c = 0; c < 4; ++c)
             if (__any_sync(0xffffffffu, valid < 32 * c + 32)) pa_mask(u[c], 32 * c, valid);
         }
-        // FP8: K's and V's scales of the chunk, one per 8 columns
-        const float4* sk = reinterpret_cast<const float4*>(scales + (chunk % kPaScales) * 32);
-        if (FP8) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const float4 f = sk[c];
-            const float g[4] = {f.x, f.y, f.z, f.w};
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float2 x = mul2(
-                  make_float2(__uint_as_float(u[c][2 * i]), __uint_as_float(u[c][2 * i + 1])),
-                  make_float2(g[i >> 2], g[i >> 2]));
-              u[c][2 * i] = __float_as_uint(x.x);
-              u[c][2 * i + 1] = __float_as_uint(x.y);
-            }
-          }
-        }
-        if (j == begin) m = pa_max32(u[0]) * sl;
+        // FP8: the chunk's scales, one of each kind per 8 columns
+        const float4* sk =
+            reinterpret_cast<const float4*>(scales + (chunk % L::kScales) * kPaScaleFloats);
+        auto largest = [&](int c) {  // scaled scores of columns 32 c ..
+          return FP8 ? pa_max32(u[c], sk[c]) : pa_max32(u[c]);
+        };
+        if (j == begin) m = largest(0) * sl;
         bool move = false;  // m moves to the maximum of this chunk too
         float2 sa, sb;
 #pragma unroll 1
         while (true) {
           if (move) {
-            const float mn = fmaxf(m, fmaxf(fmaxf(pa_max32(u[0]), pa_max32(u[1])),
-                                            fmaxf(pa_max32(u[2]), pa_max32(u[3]))) * sl);
+            const float mn =
+                fmaxf(m, fmaxf(fmaxf(largest(0), largest(1)), fmaxf(largest(2), largest(3))) * sl);
             if (j > begin) {
               // O and l scale by alpha.  O holds the products through the
               // chunk before, all complete (these scores were issued after
@@ -1101,22 +1113,42 @@ __device__ __forceinline__ void pa_softmax(const PrefillParams& p, PaBars* bars,
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             uint32_t pk[16];
-            float g[4];
-            if (FP8) {
-              const float4 f = sk[4 + c];
-              g[0] = f.x, g[1] = f.y, g[2] = f.z, g[3] = f.w;
-            }
+            if (!FP8) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float2 x = fma2(
-                  make_float2(__uint_as_float(u[c][2 * i]), __uint_as_float(u[c][2 * i + 1])), s2,
-                  n2);
-              const float2 e = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-              pk[i] = FP8 ? pack_bf16x2(e.x * g[i >> 2], e.y * g[i >> 2]) : pack_bf16x2(e.x, e.y);
-              if (i & 1)
-                sb = add2(sb, e);
-              else
-                sa = add2(sa, e);
+              for (int i = 0; i < 16; ++i) {
+                const float2 x = fma2(
+                    make_float2(__uint_as_float(u[c][2 * i]), __uint_as_float(u[c][2 * i + 1])),
+                    s2, n2);
+                const float2 e = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+                pk[i] = pack_bf16x2(e.x, e.y);
+                if (i & 1)
+                  sb = add2(sb, e);
+                else
+                  sa = add2(sa, e);
+              }
+            } else {
+              const float4 fk = sk[c], fl = sk[4 + c], fi = sk[8 + c];
+              const float gk[4] = {fk.x, fk.y, fk.z, fk.w}, gl[4] = {fl.x, fl.y, fl.z, fl.w},
+                          gi[4] = {fi.x, fi.y, fi.z, fi.w};
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const float2 a2 = make_float2(sl * gk[q], sl * gk[q]);
+                const float2 b2 = make_float2(neg + gl[q], neg + gl[q]);
+                float2 part;  // of the weights times v
+#pragma unroll
+                for (int i = 4 * q; i < 4 * q + 4; ++i) {
+                  const float2 x = fma2(
+                      make_float2(__uint_as_float(u[c][2 * i]), __uint_as_float(u[c][2 * i + 1])),
+                      a2, b2);
+                  const float2 e = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+                  pk[i] = pack_bf16x2(e.x, e.y);
+                  part = i == 4 * q ? e : add2(part, e);
+                }
+                if (q & 1)
+                  sb = fma2(part, make_float2(gi[q], gi[q]), sb);
+                else
+                  sa = fma2(part, make_float2(gi[q], gi[q]), sa);
+              }
             }
             tmem_st16(tb + kPaSCol + 16 * c, pk);
           }
@@ -1254,36 +1286,36 @@ __device__ __forceinline__ void pa_softmax(const PrefillParams& p, PaBars* bars,
         uint32_t y[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) y[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
-        if (!L::kStageOut) {
+        if constexpr (!L::kStageOut) {
           const int32_t k = out_row(r);
           if (has) pa_store_row(out0 + static_cast<int64_t>(k) * D + 32 * c, y, wide);
-          continue;
-        }
-        // Stored from its own thread, every row would touch its own lines: 32
-        // of them per instruction, some 800 cycles for 32 columns of both
-        // tiles.  64 columns at a time go through the warp's 4 KB of shared
-        // memory (16-byte chunk i of row x at i ^ (x % 8)); then eight lanes
-        // write 128 contiguous bytes of a row.
+        } else {
+          // Stored from its own thread, every row would touch its own lines: 32
+          // of them per instruction, some 800 cycles for 32 columns of both
+          // tiles.  64 columns at a time go through the warp's 4 KB of shared
+          // memory (16-byte chunk i of row x at i ^ (x % 8)); then eight lanes
+          // write 128 contiguous bytes of a row.
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(
-                           stage + lane * 128 + (((4 * (c & 1) + i) ^ (lane & 7)) << 4)),
-                       "r"(y[4 * i]), "r"(y[4 * i + 1]), "r"(y[4 * i + 2]), "r"(y[4 * i + 3])
-                       : "memory");
-        if ((c & 1) == 0) continue;
-        __syncwarp();
+          for (int i = 0; i < 4; ++i)
+            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(
+                             stage + lane * 128 + (((4 * (c & 1) + i) ^ (lane & 7)) << 4)),
+                         "r"(y[4 * i]), "r"(y[4 * i + 1]), "r"(y[4 * i + 2]), "r"(y[4 * i + 3])
+                         : "memory");
+          if ((c & 1) == 0) continue;
+          __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int x4 = 4 * i + (lane >> 3);
-          uint4 z;
-          asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                       : "=r"(z.x), "=r"(z.y), "=r"(z.z), "=r"(z.w)
-                       : "r"(stage + x4 * 128 + (((lane & 7) ^ (x4 & 7)) << 4))
-                       : "memory");
-          if (mine[i] >= 0)
-            reinterpret_cast<uint4*>(out0 + static_cast<int64_t>(mine[i]) * D + 64 * (c >> 1))[lane & 7] = z;
+          for (int i = 0; i < 8; ++i) {
+            const int x4 = 4 * i + (lane >> 3);
+            uint4 z;
+            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(z.x), "=r"(z.y), "=r"(z.z), "=r"(z.w)
+                         : "r"(stage + x4 * 128 + (((lane & 7) ^ (x4 & 7)) << 4))
+                         : "memory");
+            if (mine[i] >= 0)
+              reinterpret_cast<uint4*>(out0 + static_cast<int64_t>(mine[i]) * D + 64 * (c >> 1))[lane & 7] = z;
+          }
+          __syncwarp();
         }
-        __syncwarp();
       }
       if (!whole && (it->flags & kPaHead) && threadIdx.x == 32 * kPaSoftWarp)
         p.ws_job[blockIdx.x] = make_int4(it->job, it->row, it->h, it->nt);
@@ -1323,7 +1355,7 @@ __global__ void __launch_bounds__(PaRegs<FP8>::kThreads, 1)
       mbar_init(smem_addr(&bars->full[i]), FP8 ? 4 : 1);
       mbar_init(smem_addr(&bars->empty[i]), kPaTiles);
     }
-    for (int i = 0; i < kPaScales && FP8; ++i) {
+    for (int i = 0; i < kPaMaxCodeStages && FP8; ++i) {
       mbar_init(smem_addr(&bars->code_full[i]), 1);
       mbar_init(smem_addr(&bars->code_empty[i]), 4);
       mbar_init(smem_addr(&bars->scale_full[i]), 1);
