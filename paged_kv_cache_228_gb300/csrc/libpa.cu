@@ -1302,10 +1302,11 @@ extern "C" pa_status pa_decode_append_nvfp4(
 namespace pa {
 namespace {
 
-// The slot kernels: a cluster of kC CTAs, a programmatic dependent of the
-// work before it.
+// The slot kernels: `ctas` CTAs (a cluster of kC of them), a programmatic
+// dependent of the work before it.
 template <int kC>
-pa_status launch_slots(void (*kernel)(SlotParams), const SlotParams& p, cudaStream_t stream) {
+pa_status launch_slots(void (*kernel)(SlotParams), int ctas, const SlotParams& p,
+                       cudaStream_t stream) {
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -1314,16 +1315,19 @@ pa_status launch_slots(void (*kernel)(SlotParams), const SlotParams& p, cudaStre
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kC);
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
   cfg.blockDim = dim3(kSlThreads);
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = kC == 1 ? 1 : 2;
+  cfg.numAttrs = kC == kSlCluster ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
-// Tokens (append) or table entries (trim) from which a cluster shares them.
-constexpr int64_t kSlClusterFrom = 4096;
+// Tokens from which several CTAs share an append, and table entries (an upper
+// bound of what is released) from which a cluster shares a trim: a cluster's
+// barriers cost about 2 us, a round of 4096 tokens or blocks in one CTA 1 us.
+constexpr int64_t kSlManyTokens = 4096;
+constexpr int64_t kSlManyEntries = 1 << 17;
 
 inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
@@ -1550,9 +1554,14 @@ extern "C" pa_status pa_append_slots_device(const int32_t* lens, const int32_t* 
   p.block_size = block_size;
   p.num_blocks = num_blocks;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return num_tokens >= kSlClusterFrom
-             ? launch_slots<kSlCluster>(append_slots_kernel<kSlCluster>, p, s)
-             : launch_slots<1>(append_slots_kernel<1>, p, s);
+  if (num_tokens < kSlManyTokens) return launch_slots<1>(append_slots_kernel<1>, 1, p, s);
+  if (num_free_out == num_free || seq_lens == lens)
+    return launch_slots<kSlCluster>(append_slots_kernel<kSlCluster>, kSlCluster, p, s);
+  int sms = 0;
+  const pa_status st = device_sms(&sms, nullptr);
+  if (st != PA_OK) return st;
+  const int ctas = (num_tokens + kSlThreads - 1) / kSlThreads;
+  return launch_slots<kSlGrid>(append_slots_kernel<kSlGrid>, ctas < sms ? ctas : sms, p, s);
 }
 
 extern "C" pa_status pa_trim_slots_device(const int32_t* lens, const int32_t* new_lens,
@@ -1586,9 +1595,9 @@ extern "C" pa_status pa_trim_slots_device(const int32_t* lens, const int32_t* ne
   p.block_size = block_size;
   p.num_blocks = num_blocks;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return static_cast<int64_t>(num_seqs) * max_blocks_per_seq >= kSlClusterFrom
-             ? launch_slots<kSlCluster>(trim_slots_kernel<kSlCluster>, p, s)
-             : launch_slots<1>(trim_slots_kernel<1>, p, s);
+  return static_cast<int64_t>(num_seqs) * max_blocks_per_seq >= kSlManyEntries
+             ? launch_slots<kSlCluster>(trim_slots_kernel<kSlCluster>, kSlCluster, p, s)
+             : launch_slots<1>(trim_slots_kernel<1>, 1, p, s);
 }
 
 extern "C" pa_status pa_attention_workspace_size(int32_t num_seqs, int32_t num_q_heads,

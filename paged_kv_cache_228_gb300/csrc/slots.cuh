@@ -12,15 +12,16 @@
 // the order in which the host manager's LIFO list hands blocks out; a trim
 // pushes at F + base_b + j.
 //
-// Latency-bound: one CTA (or one cluster of 8 for long slot maps, each CTA
-// redoing the scan) walks the batch 1024 sequences at a time, one per
+// Latency-bound: each CTA walks the batch 1024 sequences at a time, one per
 // thread, keeps their records in shared memory, and then one thread per
-// token (or released block) finds its sequence by binary search there.
-// Every CTA of the cluster reads num_free and a tile's lengths before a
-// cluster barrier and rank 0 writes them after it, so both may be updated
-// in place.  Neither kernel lets its dependents start early (a decode
-// kernel reads seq_lens before it waits for its predecessor), and each
-// thread's writes are performed before it exits.
+// token (or released block) finds its sequence by binary search there, four
+// at a time so that their table loads are in flight together.  A decode
+// step's few tokens take one CTA; long slot maps take a grid, every CTA
+// redoing the scan, unless the call updates its inputs in place: then a
+// cluster of 8, whose CTAs all read num_free and a tile's lengths before a
+// cluster barrier and rank 0 writes them after it.  Neither kernel lets its
+// dependents start early (a decode kernel reads seq_lens before it waits for
+// its predecessor), and each thread's writes are performed before it exits.
 #pragma once
 
 #include <cooperative_groups.h>
@@ -32,6 +33,8 @@ namespace pa {
 constexpr int kSlThreads = 1024;
 constexpr int kSlWarps = kSlThreads / 32;
 constexpr int kSlCluster = 8;
+constexpr int kSlGrid = 0;  // CTAs without a cluster: outputs apart from the inputs
+constexpr int kSlBatch = 4;
 
 struct SlotParams {
   const int32_t* lens;
@@ -94,10 +97,10 @@ __device__ __forceinline__ void slot_scan(SlotScan& s, int64_t& a, int64_t& b, i
 
 template <int kC>
 __device__ __forceinline__ void slot_barrier() {
-  if (kC == 1)
-    __syncthreads();
-  else
+  if (kC == kSlCluster)
     cooperative_groups::this_cluster().sync();
+  else
+    __syncthreads();
 }
 
 // Index of the last of `n` ascending starts that is <= x (start[0] <= x).
@@ -119,6 +122,7 @@ __global__ void __launch_bounds__(kSlThreads) append_slots_kernel(const SlotPara
   __shared__ int32_t s_tok[kSlThreads], s_len[kSlThreads], s_base[kSlThreads];
   const int tid = threadIdx.x;
   const int rank = kC == 1 ? 0 : static_cast<int>(blockIdx.x);
+  const int64_t threads = static_cast<int64_t>(kC == 1 ? 1 : gridDim.x) * kSlThreads;
   pdl_wait();
   int32_t F = *p.num_free;
   if (F < 0 || F > p.num_blocks) {
@@ -160,28 +164,36 @@ __global__ void __launch_bounds__(kSlThreads) append_slots_kernel(const SlotPara
     // one thread per token of the tile
     const int32_t t0 = s_tok[0];
     const int32_t t1 = static_cast<int32_t>(min(tokens + tt, static_cast<int64_t>(p.num_tokens)));
-    for (int64_t x = t0 + static_cast<int64_t>(rank) * kSlThreads + tid; x < t1;
-         x += kC * kSlThreads) {
-      const int i = slot_find(s_tok, count, static_cast<int32_t>(x));
-      int64_t slot = -1;
-      if (i < fail) {
+    for (int64_t x0 = t0 + static_cast<int64_t>(rank) * kSlThreads + tid; x0 < t1;
+         x0 += kSlBatch * threads) {
+      int32_t id[kSlBatch], o[kSlBatch];
+      int32_t* fresh[kSlBatch];  // the table entry of a new block
+#pragma unroll
+      for (int q = 0; q < kSlBatch; ++q) {
+        const int64_t x = x0 + q * threads;
+        id[q] = -1;
+        o[q] = -1;
+        fresh[q] = nullptr;
+        if (x >= t1) continue;
+        const int i = slot_find(s_tok, count, static_cast<int32_t>(x));
+        if (i >= fail) continue;
         const int32_t pos = s_len[i] + static_cast<int32_t>(x) - s_tok[i];
-        const int32_t j = pos / p.block_size, o = pos - j * p.block_size;
+        const int32_t j = pos / p.block_size;
+        o[q] = pos - j * p.block_size;
         int32_t* entry = p.tables + static_cast<int64_t>(b0 + i) * p.max_blocks + j;
-        const int32_t first = (s_len[i] + p.block_size - 1) / p.block_size;
-        int32_t id;
-        if (j < first) {
-          id = *entry;
-        } else {
-          id = p.free_ids[F - 1 - (s_base[i] + j)];
-          if (o == 0) *entry = id;  // every new block's first token is a new token
-        }
-        if (id >= 0 && id < p.num_blocks)
-          slot = static_cast<int64_t>(id) * p.block_size + o;
-        else
-          flag_error(PA_DEVERR_BAD_BLOCK_ID);
+        const bool held = j < (s_len[i] + p.block_size - 1) / p.block_size;
+        id[q] = held ? *entry : p.free_ids[F - 1 - (s_base[i] + j)];
+        if (!held && o[q] == 0) fresh[q] = entry;  // a new block's first token is a new token
       }
-      p.slots[x] = slot;
+#pragma unroll
+      for (int q = 0; q < kSlBatch; ++q) {
+        const int64_t x = x0 + q * threads;
+        if (x >= t1) continue;
+        if (fresh[q] != nullptr) *fresh[q] = id[q];
+        const bool good = id[q] >= 0 && id[q] < p.num_blocks;
+        if (o[q] >= 0 && !good) flag_error(PA_DEVERR_BAD_BLOCK_ID);
+        p.slots[x] = o[q] >= 0 && good ? static_cast<int64_t>(id[q]) * p.block_size + o[q] : -1;
+      }
     }
     if (!stopped && fail < count) {
       stopped = true;
@@ -198,7 +210,7 @@ __global__ void __launch_bounds__(kSlThreads) append_slots_kernel(const SlotPara
   // rows past the last sequence have no slot
   const int64_t used = min(tokens, static_cast<int64_t>(p.num_tokens));
   for (int64_t x = used + static_cast<int64_t>(rank) * kSlThreads + tid; x < p.num_tokens;
-       x += kC * kSlThreads)
+       x += threads)
     p.slots[x] = -1;
   if (rank == 0 && tid == 0) {
     p.q_start[p.num_seqs] = static_cast<int32_t>(used);
@@ -214,6 +226,7 @@ __global__ void __launch_bounds__(kSlThreads) trim_slots_kernel(const SlotParams
   __shared__ int32_t s_at[kSlThreads], s_from[kSlThreads], s_bad[kSlThreads];
   const int tid = threadIdx.x;
   const int rank = kC == 1 ? 0 : static_cast<int>(blockIdx.x);
+  const int64_t threads = static_cast<int64_t>(kC == 1 ? 1 : gridDim.x) * kSlThreads;
   pdl_wait();
   int32_t F = *p.num_free;
   if (F < 0 || F > p.num_blocks) {
@@ -254,24 +267,34 @@ __global__ void __launch_bounds__(kSlThreads) trim_slots_kernel(const SlotParams
         slot_scan(scan, fits, none, all, unused);
       }
       __syncthreads();
-      for (int64_t x = static_cast<int64_t>(rank) * kSlThreads + tid; x < all;
-           x += kC * kSlThreads) {
-        const int i = slot_find(s_at, count, static_cast<int32_t>(x));
-        const int32_t id = p.tables[static_cast<int64_t>(b0 + i) * p.max_blocks + s_from[i] +
-                                    (static_cast<int32_t>(x) - s_at[i])];
-        if (id < 0 || id >= p.num_blocks) {
-          if (kC == 1) {
-            s_bad[i] = 1;
+      for (int64_t x0 = static_cast<int64_t>(rank) * kSlThreads + tid; x0 < all;
+           x0 += kSlBatch * threads) {
+        int32_t id[kSlBatch], at[kSlBatch];
+#pragma unroll
+        for (int q = 0; q < kSlBatch; ++q) {
+          const int32_t x = static_cast<int32_t>(x0 + q * threads);
+          id[q] = 0;
+          if (x0 + q * threads >= all) continue;
+          at[q] = slot_find(s_at, count, x);
+          id[q] = p.tables[static_cast<int64_t>(b0 + at[q]) * p.max_blocks + s_from[at[q]] +
+                           (x - s_at[at[q]])];
+        }
+#pragma unroll
+        for (int q = 0; q < kSlBatch; ++q) {
+          const int64_t x = x0 + q * threads;
+          if (x >= all) continue;
+          if (id[q] >= 0 && id[q] < p.num_blocks) {
+            p.free_ids[F + pushed + x] = id[q];
+          } else if (kC == 1) {
+            s_bad[at[q]] = 1;
             scan.redo = round + 1;
           } else {
             auto cl = cooperative_groups::this_cluster();
             for (int r = 0; r < kC; ++r) {
-              cl.map_shared_rank(s_bad, r)[i] = 1;
+              cl.map_shared_rank(s_bad, r)[at[q]] = 1;
               cl.map_shared_rank(&scan, r)->redo = round + 1;
             }
           }
-        } else {
-          p.free_ids[F + pushed + x] = id;
         }
       }
       slot_barrier<kC>();

@@ -491,10 +491,11 @@ def pa_decode_noalloc(q, k_cache, v_cache, block_tables, seq_lens, scale, out,
 
 
 # ----------------------------------------------------------- prompt side ---
-# These calls are made between short kernels, so their checks are kept to a
-# few attribute reads per tensor: 4 us instead of 20 us a call on a Grace
-# core.  Unlike the decode calls, they may be made while another device is
-# current: they run on their tensors' device.
+# These calls are made between short kernels, so what a call checks is one
+# expression of attribute reads; only where it fails are the tensors looked
+# at one by one for the message.  (10 tensors: 7 us a call on a Grace core,
+# 21 us with a helper call per check.)  Unlike the decode calls, they may be
+# made while another device is current: they run on their tensors' device.
 def _bad(t, name, dtype, shape):
     """Why `t` is not a contiguous `dtype` tensor of `shape`."""
     if t.dtype != dtype:
@@ -504,35 +505,35 @@ def _bad(t, name, dtype, shape):
     raise ValueError(f"{name}: must be contiguous")
 
 
-def _device_of(tensors, names):
-    """The index of the one CUDA device that all tensors (None: absent) are on."""
-    dev = tensors[0].get_device()
-    for t in tensors:
-        if t is not None and t.get_device() != dev or dev < 0:
-            for t, name in zip(tensors, names):
-                if t is not None and t.get_device() < 0:
-                    raise ValueError(f"{name}: must be a CUDA tensor, is on {t.device}")
-            raise ValueError("tensors on different devices: " + ", ".join(
-                f"{name} on {t.device}" for t, name in zip(tensors, names) if t is not None))
-    return dev
+def _refuse(named):
+    """Raise for the first of (name, tensor or None, dtype, shape) that is not
+    as it should be, or for tensors on the CPU or on different devices."""
+    for name, t, dtype, shape in named:
+        if t is not None and (t.dtype != dtype or tuple(t.shape) != tuple(shape) or
+                              not t.is_contiguous()):
+            _bad(t, name, dtype, shape)
+    for name, t, _, _ in named:
+        if t is not None and t.get_device() < 0:
+            raise ValueError(f"{name}: must be a CUDA tensor, is on {t.device}")
+    raise ValueError("tensors on different devices: " + ", ".join(
+        f"{name} on {t.device}" for name, t, _, _ in named if t is not None))
+
+
+_raw_stream, _current = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 
 def _call(fn, dev, stream, args):
     if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(dev)
+        stream = _raw_stream(dev)
     elif isinstance(stream, torch.cuda.Stream):
         stream = stream.cuda_stream
-    if torch._C._cuda_getDevice() == dev:
+    if _current() == dev:
         status = getattr(_lib or lib(), fn)(*args, stream)
     else:
         with torch.cuda.device(dev):
             status = getattr(_lib or lib(), fn)(*args, stream)
     if status != PA_OK:
         raise PAError(fn, status)
-
-
-_APPEND = ("lens", "n_new", "block_tables", "free_ids", "num_free", "slot_mapping", "q_start",
-           "seq_lens", "num_free_out", "num_done")
 
 
 def pa_append_slots_device(lens, n_new, block_tables, free_ids, num_free, block_size,
@@ -543,24 +544,35 @@ def pa_append_slots_device(lens, n_new, block_tables, free_ids, num_free, block_
     num_free_out may be num_free.  len(slot_mapping) is the token capacity
     (rows past the last sequence get -1)."""
     i32 = torch.int32
-    B, = lens.shape
-    N, = free_ids.shape
-    T, = slot_mapping.shape
+    of_b, of_n, of_t = lens.shape, free_ids.shape, slot_mapping.shape
+    (B,), (N,), (T,) = of_b, of_n, of_t
     width = block_tables.shape[-1]
-    tensors = (lens, n_new, block_tables, free_ids, num_free, slot_mapping, q_start, seq_lens,
-               num_free_out, num_done)
-    shapes = ((B,), (B,), (B, width), (N,), (1,), (T,), (B + 1,), (B,), (1,), (1,))
-    for t, shape, name in zip(tensors, shapes, _APPEND):
-        want = torch.int64 if t is slot_mapping else i32
-        if t.dtype is not want or t.shape != shape or not t.is_contiguous():
-            _bad(t, name, want, shape)
-    _call("pa_append_slots_device", _device_of(tensors, _APPEND), stream, (
+    dev = lens.get_device()
+    if not (dev >= 0 and lens.dtype is i32 and lens.is_contiguous() and
+            n_new.dtype is i32 and n_new.shape == of_b and n_new.is_contiguous() and
+            block_tables.dtype is i32 and block_tables.shape == (B, width) and
+            block_tables.is_contiguous() and free_ids.dtype is i32 and
+            free_ids.is_contiguous() and num_free.dtype is i32 and num_free.shape == (1,) and
+            slot_mapping.dtype is torch.int64 and slot_mapping.is_contiguous() and
+            q_start.dtype is i32 and q_start.shape == (B + 1,) and q_start.is_contiguous() and
+            seq_lens.dtype is i32 and seq_lens.shape == of_b and seq_lens.is_contiguous() and
+            num_free_out.dtype is i32 and num_free_out.shape == (1,) and
+            num_done.dtype is i32 and num_done.shape == (1,) and
+            n_new.get_device() == dev and block_tables.get_device() == dev and
+            free_ids.get_device() == dev and num_free.get_device() == dev and
+            slot_mapping.get_device() == dev and q_start.get_device() == dev and
+            seq_lens.get_device() == dev and num_free_out.get_device() == dev and
+            num_done.get_device() == dev):
+        _refuse((("lens", lens, i32, of_b), ("n_new", n_new, i32, of_b),
+                 ("block_tables", block_tables, i32, (B, width)),
+                 ("free_ids", free_ids, i32, of_n), ("num_free", num_free, i32, (1,)),
+                 ("slot_mapping", slot_mapping, torch.int64, of_t),
+                 ("q_start", q_start, i32, (B + 1,)), ("seq_lens", seq_lens, i32, of_b),
+                 ("num_free_out", num_free_out, i32, (1,)), ("num_done", num_done, i32, (1,))))
+    _call("pa_append_slots_device", dev, stream, (
         lens.data_ptr(), n_new.data_ptr(), block_tables.data_ptr(), width, free_ids.data_ptr(),
         num_free.data_ptr(), B, T, block_size, N, slot_mapping.data_ptr(), q_start.data_ptr(),
         seq_lens.data_ptr(), num_free_out.data_ptr(), num_done.data_ptr()))
-
-
-_TRIM = ("lens", "new_lens", "block_tables", "free_ids", "num_free", "seq_lens", "num_free_out")
 
 
 def pa_trim_slots_device(lens, new_lens, block_tables, free_ids, num_free, block_size, seq_lens,
@@ -568,15 +580,26 @@ def pa_trim_slots_device(lens, new_lens, block_tables, free_ids, num_free, block
     """Shrink sequence b from lens[b] to new_lens[b] tokens on the GPU: its
     blocks behind the new length are pushed onto free_ids.  seq_lens may be
     lens, num_free_out may be num_free."""
-    B, = lens.shape
-    N, = free_ids.shape
+    i32 = torch.int32
+    of_b, of_n = lens.shape, free_ids.shape
+    (B,), (N,) = of_b, of_n
     width = block_tables.shape[-1]
-    tensors = (lens, new_lens, block_tables, free_ids, num_free, seq_lens, num_free_out)
-    shapes = ((B,), (B,), (B, width), (N,), (1,), (B,), (1,))
-    for t, shape, name in zip(tensors, shapes, _TRIM):
-        if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous():
-            _bad(t, name, torch.int32, shape)
-    _call("pa_trim_slots_device", _device_of(tensors, _TRIM), stream, (
+    dev = lens.get_device()
+    if not (dev >= 0 and lens.dtype is i32 and lens.is_contiguous() and
+            new_lens.dtype is i32 and new_lens.shape == of_b and new_lens.is_contiguous() and
+            block_tables.dtype is i32 and block_tables.shape == (B, width) and
+            block_tables.is_contiguous() and free_ids.dtype is i32 and
+            free_ids.is_contiguous() and num_free.dtype is i32 and num_free.shape == (1,) and
+            seq_lens.dtype is i32 and seq_lens.shape == of_b and seq_lens.is_contiguous() and
+            num_free_out.dtype is i32 and num_free_out.shape == (1,) and
+            new_lens.get_device() == dev and block_tables.get_device() == dev and
+            free_ids.get_device() == dev and num_free.get_device() == dev and
+            seq_lens.get_device() == dev and num_free_out.get_device() == dev):
+        _refuse((("lens", lens, i32, of_b), ("new_lens", new_lens, i32, of_b),
+                 ("block_tables", block_tables, i32, (B, width)),
+                 ("free_ids", free_ids, i32, of_n), ("num_free", num_free, i32, (1,)),
+                 ("seq_lens", seq_lens, i32, of_b), ("num_free_out", num_free_out, i32, (1,))))
+    _call("pa_trim_slots_device", dev, stream, (
         lens.data_ptr(), new_lens.data_ptr(), block_tables.data_ptr(), width,
         free_ids.data_ptr(), num_free.data_ptr(), B, block_size, N, seq_lens.data_ptr(),
         num_free_out.data_ptr()))
@@ -590,56 +613,61 @@ def pa_attention_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim,
     return int(n.value)
 
 
-_ATTEND = ("q", "k_cache", "v_cache", "block_tables", "seq_lens", "out", "q_start", "workspace",
-           "k_scale", "v_scale")
-
-
 def _attention(fn, q, k_cache, v_cache, block_tables, q_start, seq_lens, scale, out, workspace,
                k_scale, v_scale, num_splits, stream):
-    bf16, i32 = torch.bfloat16, torch.int32
-    T, hq, d = q.shape
-    nb, hkv, bs, d2 = k_cache.shape
-    B, = seq_lens.shape
+    bf16, i32, f32 = torch.bfloat16, torch.int32, torch.float32
+    of_q, of_kv, of_b = q.shape, k_cache.shape, seq_lens.shape
+    T, hq, d = of_q
+    nb, hkv, bs, d2 = of_kv
+    B, = of_b
     width = block_tables.shape[-1]
-    if q.dtype is not bf16 or not q.is_contiguous():
-        _bad(q, "q", bf16, (T, hq, d))
-    if out.dtype is not bf16 or out.shape != q.shape or not out.is_contiguous():
-        _bad(out, "out", bf16, q.shape)
-    kv = _kv_dtype(k_cache)
-    if not k_cache.is_contiguous():
-        _bad(k_cache, "k_cache", k_cache.dtype, k_cache.shape)
-    if v_cache.dtype is not k_cache.dtype or v_cache.shape != k_cache.shape or \
-            not v_cache.is_contiguous():
-        _bad(v_cache, "v_cache", k_cache.dtype, k_cache.shape)
+    kv_type = k_cache.dtype
+    kv = PA_KV_BF16 if kv_type is bf16 else _kv_dtype(k_cache)
     if d2 != d:
         raise ValueError(f"{fn}: head_dim of q is {d}, of the cache {d2}")
-    if block_tables.dtype is not i32 or block_tables.shape != (B, width) or \
-            not block_tables.is_contiguous():
-        _bad(block_tables, "block_tables", i32, (B, width))
-    if seq_lens.dtype is not i32 or not seq_lens.is_contiguous():
-        _bad(seq_lens, "seq_lens", i32, (B,))
-    if q_start is not None and (q_start.dtype is not i32 or q_start.shape != (B + 1,) or
-                                not q_start.is_contiguous()):
-        _bad(q_start, "q_start", i32, (B + 1,))
+    dev = q.get_device()
+    ok = (dev >= 0 and q.dtype is bf16 and q.is_contiguous() and
+          out.dtype is bf16 and out.shape == of_q and out.is_contiguous() and
+          k_cache.is_contiguous() and v_cache.dtype is kv_type and v_cache.shape == of_kv and
+          v_cache.is_contiguous() and block_tables.dtype is i32 and
+          block_tables.shape == (B, width) and block_tables.is_contiguous() and
+          seq_lens.dtype is i32 and seq_lens.is_contiguous() and
+          k_cache.get_device() == dev and v_cache.get_device() == dev and
+          block_tables.get_device() == dev and seq_lens.get_device() == dev and
+          out.get_device() == dev)
+    starts = ks = vs = ws = None
+    ws_bytes = 0
+    if q_start is not None:
+        ok = ok and (q_start.dtype is i32 and q_start.shape == (B + 1,) and
+                     q_start.is_contiguous() and q_start.get_device() == dev)
+        starts = q_start.data_ptr()
+    if workspace is not None:
+        ok = ok and workspace.is_contiguous() and workspace.get_device() == dev
+        ws, ws_bytes = workspace.data_ptr(), workspace.nbytes
     if kv == PA_KV_FP8_E4M3:
-        for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-            if t is None:
-                raise ValueError(f"{fn}: an FP8 cache needs {name}")
-            if t.dtype is not torch.float32 or t.shape != (nb, hkv) or not t.is_contiguous():
-                _bad(t, name, torch.float32, (nb, hkv))
+        if k_scale is None or v_scale is None:
+            raise ValueError(f"{fn}: an FP8 cache needs k_scale and v_scale")
+        ok = ok and (k_scale.dtype is f32 and k_scale.shape == (nb, hkv) and
+                     k_scale.is_contiguous() and k_scale.get_device() == dev and
+                     v_scale.dtype is f32 and v_scale.shape == (nb, hkv) and
+                     v_scale.is_contiguous() and v_scale.get_device() == dev)
+        ks, vs = k_scale.data_ptr(), v_scale.data_ptr()
     elif k_scale is not None or v_scale is not None:
         raise ValueError(f"{fn}: a bf16 cache takes no scales")
-    if workspace is not None and not workspace.is_contiguous():
-        raise ValueError("workspace: must be contiguous")
-    dev = _device_of((q, k_cache, v_cache, block_tables, seq_lens, out, q_start, workspace,
-                      k_scale, v_scale), _ATTEND)
+    if not ok:
+        named = [("q", q, bf16, of_q), ("k_cache", k_cache, kv_type, of_kv),
+                 ("v_cache", v_cache, kv_type, of_kv),
+                 ("block_tables", block_tables, i32, (B, width)),
+                 ("seq_lens", seq_lens, i32, of_b), ("out", out, bf16, of_q),
+                 ("q_start", q_start, i32, (B + 1,)), ("k_scale", k_scale, f32, (nb, hkv)),
+                 ("v_scale", v_scale, f32, (nb, hkv))]
+        if workspace is not None:
+            named.append(("workspace", workspace, workspace.dtype, workspace.shape))
+        _refuse(named)
     _call(fn, dev, stream, (
-        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-        None if k_scale is None else k_scale.data_ptr(),
-        None if v_scale is None else v_scale.data_ptr(), kv, block_tables.data_ptr(), width,
-        None if q_start is None else q_start.data_ptr(), seq_lens.data_ptr(), B, T, hq, hkv, d,
-        bs, nb, float(scale), out.data_ptr(), None if workspace is None else workspace.data_ptr(),
-        0 if workspace is None else workspace.nbytes, num_splits))
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), ks, vs, kv,
+        block_tables.data_ptr(), width, starts, seq_lens.data_ptr(), B, T, hq, hkv, d, bs, nb,
+        float(scale), out.data_ptr(), ws, ws_bytes, num_splits))
 
 
 def pa_prefill(q, k_cache, v_cache, block_tables, q_start, seq_lens, scale, out, workspace=None,

@@ -168,7 +168,7 @@ def test_bad_ids_are_flagged():
 
 def test_bad_ids_in_a_cluster_trim():
     # wide tables take the 8-CTA form; bad entries in several sequences
-    B, bs, width = 300, 8, 40
+    B, bs, width = 300, 8, 500
     dev = Device(BM.BlockManagerModel(B * 12), B, width, bs)
     dev.append(_i32([90] * B), 90 * B)
     before = dev.tab[:, :12].clone()
@@ -196,6 +196,29 @@ def test_separate_outputs_repeat():
         got.append((slots.tolist(), start.tolist(), lens.tolist(), nf.tolist()))
     assert got[0] == got[1] and got[0][3] == [95]
     assert int(dev.num_free) == 100 and dev.lens.tolist() == [0, 0, 0]
+
+
+@pytest.mark.parametrize("B,top", [(60, 300), (1100, 30)])
+def test_long_maps_with_separate_outputs(B, top):
+    # outputs apart from the inputs: the slot map is shared by a whole grid
+    rng = np.random.default_rng(B)
+    n_new = rng.integers(0, top, B).tolist()
+    assert sum(n_new) > 4096
+    model = BM.BlockManagerModel(sum(n_new))
+    dev = Device(model, B, 64, 8)
+    slots = torch.empty(sum(n_new), dtype=torch.int64, device="cuda")
+    start, lens, nf = _i32([0] * (B + 1)), _i32([0] * B), _i32([0])
+    pa.pa_append_slots_device(dev.lens, _i32(n_new), dev.tab, dev.free, dev.num_free, 8, slots,
+                              start, lens, nf, dev.done)
+    tables, want = [[] for _ in range(B)], []
+    for b in range(B):
+        _, s, _ = model.append_slots(tables[b], 0, n_new[b], 8, 64)
+        want += s
+    assert slots.tolist() == want and lens.tolist() == n_new and dev.done.tolist() == [B]
+    assert int(nf) == len(model.free_stack)
+    got = dev.tab.tolist()
+    assert all(got[b][:len(t)] == t for b, t in enumerate(tables))
+    assert pa.pa_get_device_error() == 0
 
 
 def test_captured_steps_advance_in_place():
