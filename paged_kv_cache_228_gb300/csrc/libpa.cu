@@ -1327,7 +1327,7 @@ pa_status launch_slots(void (*kernel)(SlotParams), int ctas, const SlotParams& p
 // bound of what is released) from which a cluster shares a trim: a cluster's
 // barriers cost about 2 us, a round of 4096 tokens or blocks in one CTA 1 us.
 constexpr int64_t kSlManyTokens = 4096;
-constexpr int64_t kSlManyEntries = 1 << 17;
+constexpr int64_t kSlManyEntries = 1 << 19;
 
 inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
