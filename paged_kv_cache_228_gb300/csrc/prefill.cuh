@@ -69,7 +69,6 @@ constexpr int kPaChunk = 128;          // tokens per chunk
 constexpr int kPaWarps = 12;
 constexpr int kPaThreads = 32 * kPaWarps;
 constexpr int kPaSoftWarp = 4;
-constexpr int kPaSoftWarps = 8;
 constexpr int kPaConvWarp = kPaWarps;
 // Registers per thread.  The launch gives every thread the same (65536 over
 // the threads, in steps of 8); the other warpgroups then give up some to the
@@ -103,19 +102,14 @@ struct PaSmem {
   static constexpr int kKV = kPaChunk * D * 2;  // K (or V) of a chunk, bf16
   static constexpr int kCodes = kPaChunk * D;   // the same as E4M3
   // one ring: K_j, V_j, K_j+1, ...; FP8 has a second one of codes before it
-  static constexpr int kStages = FP8 ? (D == 64 ? 8 : 4) : (D == 64 ? 10 : 4);
-  static constexpr int kCodeStages = FP8 ? (D == 64 ? 3 : 2) : 0;
-  // 4 KB per softmax warp to turn rows into whole lines on their way out; not
-  // where the codes' ring leaves no room
-  static constexpr bool kStageOut = !FP8 || D == 64;
-  static constexpr bool kDual = kStages >= 8;
+  static constexpr int kStages = FP8 ? (D == 64 ? 8 : 4) : (D == 64 ? 12 : 5);
+  static constexpr int kCodeStages = FP8 ? (D == 64 ? 7 : 2) : 0;
   static constexpr int kQ = kPaRows * D * 2;    // one query tile
   static constexpr int kOffRing = kPaTiles * kQ;
   static constexpr int kOffCodes = kOffRing + kStages * kKV;
   static constexpr int kOffMl = kOffCodes + kCodeStages * kCodes;  // tile 1's (m, l), folded by tile 0
-  static constexpr int kOffOut = kOffMl + kPaRows * 8;
   static constexpr int kScales = D == 64 ? 8 : 4;  // chunks whose FP8 scales are kept
-  static constexpr int kOffScale = kOffOut + (kStageOut ? kPaSoftWarps * 4096 : 0);  
+  static constexpr int kOffScale = kOffMl + kPaRows * 8;
   static constexpr int kOffBar = kOffScale + (FP8 ? kScales * kPaScaleFloats * 4 : 0);
   static constexpr int kBytes = kOffBar + kPaBarBytes;
   static constexpr int kGroup = D * 16;         // 8 tokens: D / 64 slabs of 8 x 128 bytes
@@ -277,9 +271,7 @@ __device__ __forceinline__ uint32_t pa_units(const PrefillParams& p, const PaSeq
                        static_cast<uint32_t>(s.off) + p.tok_per_item + (kPaChunk - 1));
 }
 
-// The walk over a CTA's items.  kDual: the ring is deep enough for chunks of
-// both tiles' own (head_dim 64).
-template <bool kDual>
+// The walk over a CTA's items.
 struct PaWalk {
   uint32_t lo, hi, u;  // the CTA's units; the current item's first unit
   int32_t b, h, i;    // sequence, KV head, item of the head
@@ -324,7 +316,7 @@ struct PaWalk {
   // t takes every other chunk from j0 + t, and tile 0 folds the two at the
   // end.
   __device__ __forceinline__ bool dual(const PrefillParams& p) const {
-    return kDual && nt <= p.tok_per_tile && j1 - j0 >= 2;
+    return nt <= p.tok_per_tile && j1 - j0 >= 2;
   }
   // the end of tile t's chunks: past its last row's limit there are none
   __device__ __forceinline__ int32_t tile_end(const PrefillParams& p, int t) const {
@@ -334,9 +326,10 @@ struct PaWalk {
   }
 };
 
-// The plan, first part, every thread: the units of its sequences, thread t
-// taking [B t / 384, B (t + 1) / 384).  The launch makes sure that the whole
-// batch's units stay below 2^32.
+// The plan.  The launch makes sure that the whole batch's units stay below
+// 2^32.  A batch of at most 32 sequences is planned by one warp, a sequence
+// per lane; larger ones have a first part in which every thread adds up the
+// units of its sequences, thread t taking [B t / 384, B (t + 1) / 384).
 __device__ __forceinline__ int32_t pa_first_seq(const PrefillParams& p, int t) {
   return static_cast<int32_t>(static_cast<int64_t>(p.num_seqs) * t / kPaThreads);
 }
@@ -369,66 +362,76 @@ __device__ __forceinline__ uint32_t pa_share(uint32_t units, uint32_t parts, uin
   return q * c + rest * c / parts;
 }
 
-// Second part, one warp: this CTA's range and its first item.  `sums`: the
-// threads' units.  Returns false when the CTA has nothing to do.
-template <bool kDual>
+// One warp: this CTA's range and its first item.  `sums`: the threads' units
+// of a batch of more than 32 sequences.  Returns false when the CTA has
+// nothing to do.
 __device__ __forceinline__ bool pa_plan(const PrefillParams& p, PaBars* bars,
-                                        const uint32_t* sums, PaWalk<kDual>& w, uint32_t& units,
+                                        const uint32_t* sums, PaWalk& w, uint32_t& units,
                                         uint32_t& parts) {
   const int lane = threadIdx.x & 31;
-  if (bars->bad) return false;
-  // lane i holds the units of threads [12 i, 12 i + 12)
   constexpr int kPer = kPaThreads / 32;
-  uint32_t mine = 0;
+  const bool small = p.num_seqs <= 32;
+  PaSeq s = {0, 0, 0, 0, 0};
+  uint32_t head = 0, mine = 0;  // units of a KV head of the lane's sequence, of all its sequences
+  if (small) {
+    bool bad = false;
+    if (lane < p.num_seqs) s = pa_seq(p, lane, bad, blockIdx.x == 0);
+    if (__any_sync(0xffffffffu, bad)) return false;
+    head = pa_units(p, s, s.items);
+    mine = head * p.num_kv_heads;
+  } else {
+    if (bars->bad) return false;
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) mine += sums[lane * kPer + i];
+    for (int i = 0; i < kPer; ++i) mine += sums[lane * kPer + i];  // threads [12 lane, + 12)
+  }
   const uint32_t incl = pa_warp_sum(mine);
   units = __shfl_sync(0xffffffffu, incl, 31);
   // no more ranges than two units each: a one-chunk item stays whole
   parts = max(1u, min(units / (kPaItemCost + 1), static_cast<uint32_t>(p.num_ctas)));
   const uint32_t c = blockIdx.x;
   if (c >= parts) return false;
-  w.lo = pa_share(units, parts, c);
-  w.hi = pa_share(units, parts, c + 1);
+  const uint32_t q = units / parts, rest = units - q * parts;  // as pa_share
+  w.lo = q * c + rest * c / parts;
+  w.hi = q * (c + 1) + rest * (c + 1) / parts;
   if (w.lo >= w.hi) return false;
-  // the thread whose sequences hold unit lo
+  // the sequence that holds unit lo
   const int li = __ffs(__ballot_sync(0xffffffffu, w.lo < incl)) - 1;
   uint32_t at = __shfl_sync(0xffffffffu, incl - mine, li);
-  int t = li * kPer;
+  if (small) {
+    w.b = li;
+    w.s.q0 = __shfl_sync(0xffffffffu, s.q0, li);
+    w.s.nq = __shfl_sync(0xffffffffu, s.nq, li);
+    w.s.n = __shfl_sync(0xffffffffu, s.n, li);
+    w.s.off = __shfl_sync(0xffffffffu, s.off, li);
+    w.s.items = __shfl_sync(0xffffffffu, s.items, li);
+    head = __shfl_sync(0xffffffffu, head, li);
+  } else {
+    int t = li * kPer;
 #pragma unroll 1
-  for (; t < kPaThreads - 1 && w.lo >= at + sums[t]; ++t) at += sums[t];
-  // then its sequence and the KV head (a first round with all the items of a
-  // head), then the head's last item that starts at or before the rest y,
-  // 32 candidates a round
-  w.b = pa_first_seq(p, t);
-  uint32_t y = w.lo - at, start = 0;
-  int32_t a = 0, e = 0;
-  bool found = false;
+    for (; t < kPaThreads - 1 && w.lo >= at + sums[t]; ++t) at += sums[t];
+    w.b = pa_first_seq(p, t);
 #pragma unroll 1
-  while (!found || e - a > 1) {
-    if (!found) {
+    while (true) {
       if (w.b >= p.num_seqs) return false;  // lengths changed under the call
       bool bad;
       w.s = pa_seq(p, w.b, bad, false);
-      e = w.s.items;
+      head = pa_units(p, w.s, w.s.items);
+      if (w.lo - at < head * p.num_kv_heads) break;
+      at += head * p.num_kv_heads;
+      ++w.b;
     }
-    const int32_t step = (e - a + 31) / 32;
-    const int32_t k = found ? min(a + lane * step, e) : e;
+  }
+  // the KV head, then its last item that starts at or before the rest y, 32
+  // candidates a round
+  uint32_t y = w.lo - at, start = 0;
+  w.h = y / head;
+  y -= w.h * head;
+  at += w.h * head;
+  int32_t a = 0, e = w.s.items;
+#pragma unroll 1
+  while (e - a > 1) {
+    const int32_t step = (e - a + 31) / 32, k = min(a + lane * step, e);
     const uint32_t before = pa_units(p, w.s, k);
-    if (!found) {
-      const uint32_t all = before * p.num_kv_heads;
-      if (y >= all) {  // not in this sequence
-        y -= all;
-        at += all;
-        ++w.b;
-        continue;
-      }
-      found = true;
-      w.h = y / before;
-      y -= w.h * before;
-      at += w.h * before;
-      continue;
-    }
     const int last = 31 - __clz(__ballot_sync(0xffffffffu, k < e && before <= y));
     start = __shfl_sync(0xffffffffu, before, last);  // lane 0 always qualifies
     a += last * step;
@@ -696,7 +699,7 @@ __device__ __forceinline__ void pa_items(const PrefillParams& p, PaBars* bars,
                                          const CUtensorMap* tm_q, uint32_t sq,
                                          const uint32_t* sums) {
   using L = PaSmem<D, FP8>;
-  PaWalk<L::kDual> w;
+  PaWalk w;
   uint32_t units, parts;
   const bool work = pa_plan(p, bars, sums, w, units, parts);
   const int lane = threadIdx.x & 31;
@@ -861,10 +864,10 @@ __device__ __forceinline__ void pa_mma(const PrefillParams& p, PaBars* bars, int
     if (leader && it->j1 > it->j0) {
       const int32_t j0 = it->j0, j1 = it->j1, end0 = it->end[0], end1 = it->end[1];
       const int32_t end = t == 0 ? end0 : end1;
-      const bool dual = L::kDual && (it->flags & kPaDual);
+      const bool dual = (it->flags & kPaDual) != 0;
       const int32_t step = dual ? 2 : 1;
       // turns of the item: chunks that both tiles have
-      const int32_t both = dual ? (j1 - j0) / 2 : min(end0, end1) - j0;
+      const int32_t both = dual ? 0 : min(end0, end1) - j0;
       int32_t j = j0;
       if (dual && t == 1) {
         pass();
@@ -897,13 +900,7 @@ __device__ __forceinline__ void pa_mma(const PrefillParams& p, PaBars* bars, int
         ok = full();
         const uint32_t vst = r.stage, vb = ring + vst * L::kKV;
         r.advance();
-        if (more) {
-          if (dual) {  // the other tile's chunk lies between
-            pass();
-            pass();
-          }
-          ok = ok && full();
-        }
+        if (more && !dual) ok = ok && full();
         ok = ok && pa_wait(smem_addr(&bars->p_full[t]), pph);
         pph ^= 1u;
         // tile 0's turn n comes behind tile 1's n - 1, tile 1's behind tile 0's n
@@ -919,21 +916,33 @@ __device__ __forceinline__ void pa_mma(const PrefillParams& p, PaBars* bars, int
           umma_bf16_ta(tt + kPaOCol, tt + kPaSCol + k * 8,
                        smem_desc_sw128(vb + k * 2 * L::kGroup, 1024, L::kGroup), kIdPV,
                        n > 0 || k > 0);
+        if (dual) {
+          // V_j goes back before the wait for K_j+2: the other tile's chunk
+          // lies between them in the ring
+          umma_commit(smem_addr(&bars->empty[vst]));
+          if (more) {
+            pass();
+            pass();
+            ok = ok && full();
+            if (!ok) break;
+            tc_fence_after_sync();
+          }
+        }
         if (more) scores();
         if (n < both) mbar_arrive(smem_addr(&bars->turn[1 - t]));
         if (more) {
           umma_commit(smem_addr(&bars->s_full[t]));
           if (j + 2 * step >= end) umma_commit(smem_addr(&bars->q_free[t]));
-          umma_commit(smem_addr(&bars->empty[vst]));
+          if (!dual) umma_commit(smem_addr(&bars->empty[vst]));
           umma_commit(smem_addr(&bars->empty[r.stage]));
           r.advance();
         } else {
           umma_commit(smem_addr(&bars->o_last[t]));
-          umma_commit(smem_addr(&bars->empty[vst]));
+          if (!dual) umma_commit(smem_addr(&bars->empty[vst]));
         }
       }
       // tile 1's last turn, where tile 0 has no further chunk of its own
-      if (t == 0 && both > 0 && end - j0 <= both * step) owed = true;
+      if (t == 0 && both > 0 && end - j0 <= both) owed = true;
       // chunks behind the tile's last one
       if (dual) j -= 1;
       for (; j < j1 && ok; ++j) {
@@ -1023,7 +1032,7 @@ __device__ __forceinline__ void pa_store_row(__nv_bfloat16* dst, const uint32_t 
 template <int D, bool FP8>
 __device__ __forceinline__ void pa_softmax(const PrefillParams& p, PaBars* bars, int tile,
                                            uint32_t tmem, uint32_t ring, float2* s_ml,
-                                           const float* scales, uint32_t stage) {
+                                           const float* scales) {
   using L = PaSmem<D, FP8>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int quarter = warp & 3;       // tensor-memory lanes 32 * quarter ...
@@ -1043,7 +1052,7 @@ __device__ __forceinline__ void pa_softmax(const PrefillParams& p, PaBars* bars,
       break;
     }
     if (it->flags & kPaEnd) break;
-    const bool dual = L::kDual && (it->flags & kPaDual);
+    const bool dual = (it->flags & kPaDual) != 0;
     const int32_t j0 = it->j0, begin = j0 + (dual ? tile : 0), step = dual ? 2 : 1;
     const int32_t end = it->end[tile], n = it->n;
     const int32_t tk = rt + (dual ? 0 : tile * p.tok_per_tile);  // the row's token of the item
@@ -1229,21 +1238,9 @@ __device__ __forceinline__ void pa_softmax(const PrefillParams& p, PaBars* bars,
       // slot 0 (it is then the CTA's first item)
       const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (it->flags & kPaHead ? 1 : 0);
       float4* po = reinterpret_cast<float4*>(p.ws_o) + slot * (D / 4) * kPaItemRows + row;
-      // out row of row x of the tile, -1 where it has none
-      const int32_t nt = it->nt, tk0 = dual ? 0 : tile * p.tok_per_tile;
-      auto out_row = [&](int32_t x) -> int32_t {
-        const int32_t xt = static_cast<int32_t>(pa_div(p, static_cast<uint32_t>(x)));
-        return xt < p.tok_per_tile && xt + tk0 < nt
-                   ? (xt + tk0) * p.num_q_heads + (x - xt * p.group)
-                   : -1;
-      };
-      int32_t mine[8];  // of the rows that this lane writes
-      if (L::kStageOut) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) mine[i] = out_row(32 * quarter + 4 * i + (lane >> 3));
-      }
-      __nv_bfloat16* out0 =
-          p.out + (static_cast<int64_t>(it->row) * p.num_q_heads + it->h * p.group) * D;
+      __nv_bfloat16* to =
+          p.out + (static_cast<int64_t>(it->row + tk) * p.num_q_heads + it->h * p.group +
+                   (r - rt * p.group)) * D;
       if (!whole && has) p.ws_ml[slot * kPaItemRows + row] = make_float2(m, l);
       if (whole) {
         const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -1274,47 +1271,17 @@ __device__ __forceinline__ void pa_softmax(const PrefillParams& p, PaBars* bars,
 #pragma unroll
           for (int i = 0; i < 32; ++i) x[i] = 0.f;
         }
+        if (!has) continue;
         if (!whole) {
-          if (has) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              po[(8 * c + i) * kPaItemRows] =
-                  make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-          }
-          continue;
-        }
-        uint32_t y[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) y[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
-        if constexpr (!L::kStageOut) {
-          const int32_t k = out_row(r);
-          if (has) pa_store_row(out0 + static_cast<int64_t>(k) * D + 32 * c, y, wide);
+          for (int i = 0; i < 8; ++i)
+            po[(8 * c + i) * kPaItemRows] =
+                make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
         } else {
-          // Stored from its own thread, every row would touch its own lines: 32
-          // of them per instruction, some 800 cycles for 32 columns of both
-          // tiles.  64 columns at a time go through the warp's 4 KB of shared
-          // memory (16-byte chunk i of row x at i ^ (x % 8)); then eight lanes
-          // write 128 contiguous bytes of a row.
+          uint32_t y[16];
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(
-                             stage + lane * 128 + (((4 * (c & 1) + i) ^ (lane & 7)) << 4)),
-                         "r"(y[4 * i]), "r"(y[4 * i + 1]), "r"(y[4 * i + 2]), "r"(y[4 * i + 3])
-                         : "memory");
-          if ((c & 1) == 0) continue;
-          __syncwarp();
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int x4 = 4 * i + (lane >> 3);
-            uint4 z;
-            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                         : "=r"(z.x), "=r"(z.y), "=r"(z.z), "=r"(z.w)
-                         : "r"(stage + x4 * 128 + (((lane & 7) ^ (x4 & 7)) << 4))
-                         : "memory");
-            if (mine[i] >= 0)
-              reinterpret_cast<uint4*>(out0 + static_cast<int64_t>(mine[i]) * D + 64 * (c >> 1))[lane & 7] = z;
-          }
-          __syncwarp();
+          for (int i = 0; i < 16; ++i) y[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+          pa_store_row(to + 32 * c, y, wide);
         }
       }
       if (!whole && (it->flags & kPaHead) && threadIdx.x == 32 * kPaSoftWarp)
@@ -1393,13 +1360,15 @@ __global__ void __launch_bounds__(PaRegs<FP8>::kThreads, 1)
   pdl_wait();  // launched as a programmatic dependent: inputs ready below
   pdl_trigger();
 
+  if (threadIdx.x == 32 * kPaSoftWarp) p.ws_job[blockIdx.x] = make_int4(0, 0, 0, 0);
   // the threads' units, where the ring will be: the copies start behind the
   // first item's record, which warp 1 writes after it has read them
   uint32_t* sums = reinterpret_cast<uint32_t*>(pa_smem + L::kOffRing);
-  if (!FP8 || threadIdx.x < kPaThreads) sums[threadIdx.x] = pa_thread_units(p, bars);
-  fence_proxy_async_smem();
-  if (threadIdx.x == 32 * kPaSoftWarp) p.ws_job[blockIdx.x] = make_int4(0, 0, 0, 0);
-  __syncthreads();
+  if (p.num_seqs > 32) {
+    if (!FP8 || threadIdx.x < kPaThreads) sums[threadIdx.x] = pa_thread_units(p, bars);
+    fence_proxy_async_smem();
+    __syncthreads();
+  }
   using R = PaRegs<FP8>;
   float* scales = reinterpret_cast<float*>(pa_smem + L::kOffScale);
   if (warp < kPaSoftWarp) {
@@ -1413,8 +1382,7 @@ __global__ void __launch_bounds__(PaRegs<FP8>::kThreads, 1)
   } else if (!FP8 || warp < kPaConvWarp) {
     regs_inc<R::kSoft>();
     pa_softmax<D, FP8>(p, bars, (warp - kPaSoftWarp) >> 2, tmem, ring,
-                       reinterpret_cast<float2*>(pa_smem + L::kOffMl), scales,
-                       base + L::kOffOut + (warp - kPaSoftWarp) * 4096);
+                       reinterpret_cast<float2*>(pa_smem + L::kOffMl), scales);
   } else {
     if constexpr (FP8) {
       regs_dec<R::kConv>();
