@@ -103,7 +103,7 @@ struct PaSmem {
   static constexpr int kCodes = kPaChunk * D;   // the same as E4M3
   // one ring: K_j, V_j, K_j+1, ...; FP8 has a second one of codes before it
   static constexpr int kStages = FP8 ? (D == 64 ? 8 : 4) : (D == 64 ? 12 : 5);
-  static constexpr int kCodeStages = FP8 ? (D == 64 ? 7 : 2) : 0;
+  static constexpr int kCodeStages = FP8 ? (D == 64 ? 6 : 2) : 0;
   static constexpr int kQ = kPaRows * D * 2;    // one query tile
   static constexpr int kOffRing = kPaTiles * kQ;
   static constexpr int kOffCodes = kOffRing + kStages * kKV;
@@ -114,8 +114,10 @@ struct PaSmem {
   static constexpr int kBytes = kOffBar + kPaBarBytes;
   static constexpr int kGroup = D * 16;         // 8 tokens: D / 64 slabs of 8 x 128 bytes
   static_assert(kStages <= kPaMaxStages && kBytes <= 227 * 1024, "shared memory");
-  // the copies run at most both rings ahead of the softmax
-  static_assert(!FP8 || kStages + kCodeStages <= 2 * kScales - 1, "scale ring");
+  // The copies run ahead of the products by both rings and the one slot that
+  // the widening warps hold in registers: when they write a chunk's scales,
+  // the products of the chunk that had the place before are done.
+  static_assert(!FP8 || kStages + kCodeStages + 1 <= 2 * kScales - 1, "scale ring");
 };
 
 // One item as the walk hands it to the other warps.

@@ -91,6 +91,31 @@ def test_work_partitions(splits, fp8):
     _check(c, False, f"cross splits {splits}", splits=splits)
 
 
+@pytest.mark.parametrize("fp8", FP8)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("splits", [1, 3, 0])
+def test_long_runs_through_the_rings(splits, d, fp8):
+    # every ring goes round many times in one CTA: items of one tile (both
+    # tiles take chunks in turn), of two, and of one chunk, behind each other
+    news = [1, 3, 70, 200, 1, 64, 2]
+    lens = [3000, 100, 2500, 200, 1500, 1700, 129]
+    c = Prompt(news, lens, 4, 1, d, 16, seed=20, fp8=fp8)
+    _check(c, True, "causal", splits=splits)
+    _check(c, False, "cross", splits=splits)
+
+
+@pytest.mark.parametrize("fp8", FP8)
+@pytest.mark.parametrize("d", [64, 128])
+def test_many_one_token_sequences_with_offsets(d, fp8):
+    # a batch of more than 32 sequences, each an item of one tile over several
+    # chunks
+    rng = np.random.default_rng(21)
+    lens = rng.integers(1, 2000, 64).tolist()
+    c = Prompt([1] * 64, lens, 4, 2, d, 32, seed=21, fp8=fp8)
+    for _ in range(3):
+        _check(c, False, "one token each")
+
+
 def test_partition_does_not_depend_on_blocks_and_repeats_bit_for_bit():
     c = Prompt([40, 300], [900, 300], 8, 2, 128, 16, seed=4)
     a, b = _run(c, True), _run(c, True)
