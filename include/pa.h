@@ -597,9 +597,8 @@ pa_status pa_prefill(const void* q, const void* k_cache, const void* v_cache,
  * without the causal limit.  Every query token of sequence b sees all
  * seq_lens[b] encoder states; none (0) gives zeros.  Sequences may share
  * encoder blocks through their tables.  q_start == NULL is the decode step,
- * one token per sequence (num_tokens == num_seqs); with at most 8 query
- * heads per KV head that step runs pa_decode's kernels, and seq_lens is then
- * read early, as there. */
+ * one token per sequence (num_tokens == num_seqs); batches of it run
+ * pa_decode's kernels, and seq_lens is then read early, as there. */
 pa_status pa_cross_attention(const void* q, const void* k_cache, const void* v_cache,
                              const float* k_scale, const float* v_scale,
                              pa_kv_dtype kv_dtype, const int32_t* block_tables,

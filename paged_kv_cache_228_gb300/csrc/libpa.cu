@@ -1469,7 +1469,14 @@ pa_status attention_entry(bool causal, const void* q, const void* k_cache, const
   if (items * num_kv_heads > INT_MAX ||
       items * num_kv_heads * (chunks + kPaItemCost) > 0xffffffffll - (1 << 20))
     return PA_ERR_UNSUPPORTED;
-  if (q_start == nullptr && group <= kMaxG)
+  // One token a sequence: the decode kernels, whose rows fit the batch, but
+  // for one or two sequences over long tables the wider split of the kernel
+  // here (one of 2000 tokens, 32 / 8 heads: bf16 d 128 12.7 against 21.1 us,
+  // FP8 d 64 14.8 against 22.5; four 14.2 against 15.8; 200 tokens 9.6 against
+  // 7.9).  FP8 at d 128 decodes on tcgen05 (9.8 against 16.8).
+  const bool few = num_seqs <= 2 && max_blocks_per_seq >= 1024 / block_size &&
+                   !(kv_dtype == PA_KV_FP8_E4M3 && head_dim == 128);
+  if (q_start == nullptr && group <= kMaxG && !few)
     return decode_entry(q, k_cache, v_cache, k_scale, v_scale, kv_dtype, block_tables,
                         max_blocks_per_seq, seq_lens, num_seqs, num_q_heads, num_kv_heads,
                         head_dim, block_size, num_blocks, scale, out, workspace, workspace_bytes,
