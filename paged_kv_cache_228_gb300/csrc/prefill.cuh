@@ -843,7 +843,8 @@ __device__ __forceinline__ void pa_mma(const PrefillParams& p, PaBars* bars, int
   constexpr uint32_t kIdPV = idesc_bf16(kPaRows, D, false, true);
   const bool leader = (threadIdx.x & 31) == 0;
   const uint32_t tt = tmem + t * kPaTileCols;
-  const uint32_t qb = sq + t * L::kQ;
+  // the descriptors' address field counts 16 bytes: later operands are sums
+  const uint64_t qd = smem_desc_sw128(sq + t * L::kQ, 16, 1024);
   PaItems items;
   PaRing<L::kStages> r;
   uint32_t qph = 0, pph = 0, tph = 0;  // parity of the next queries, P, turn
@@ -877,13 +878,11 @@ __device__ __forceinline__ void pa_mma(const PrefillParams& p, PaBars* bars, int
         ++j;
       }
       auto scores = [&]() {  // of the chunk whose K is the next stage
-        const uint32_t kb = ring + r.stage * L::kKV;
+        const uint64_t kd = smem_desc_sw128(ring + r.stage * L::kKV, 16, L::kGroup);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
-          umma_bf16(tt + kPaSCol,
-                    smem_desc_sw128(qb + (k >> 2) * (kPaRows * 128) + (k & 3) * 32, 16, 1024),
-                    smem_desc_sw128(kb + (k >> 2) * 1024 + (k & 3) * 32, 16, L::kGroup), kIdQK,
-                    k > 0);
+          umma_bf16(tt + kPaSCol, qd + (((k >> 2) * (kPaRows * 128) + (k & 3) * 32) >> 4),
+                    kd + (((k >> 2) * 1024 + (k & 3) * 32) >> 4), kIdQK, k > 0);
       };
       if (j < end && ok) {
         ok = full() && pa_wait(smem_addr(&bars->q_full[t]), qph);
@@ -900,7 +899,8 @@ __device__ __forceinline__ void pa_mma(const PrefillParams& p, PaBars* bars, int
       for (int32_t n = 0; j < end && ok; j += step, ++n) {
         const bool more = j + step < end;
         ok = full();
-        const uint32_t vst = r.stage, vb = ring + vst * L::kKV;
+        const uint32_t vst = r.stage;
+        const uint64_t vd = smem_desc_sw128(ring + vst * L::kKV, 1024, L::kGroup);
         r.advance();
         if (more && !dual) ok = ok && full();
         ok = ok && pa_wait(smem_addr(&bars->p_full[t]), pph);
@@ -915,8 +915,7 @@ __device__ __forceinline__ void pa_mma(const PrefillParams& p, PaBars* bars, int
         tc_fence_after_sync();
 #pragma unroll
         for (int k = 0; k < kPaChunk / 16; ++k)
-          umma_bf16_ta(tt + kPaOCol, tt + kPaSCol + k * 8,
-                       smem_desc_sw128(vb + k * 2 * L::kGroup, 1024, L::kGroup), kIdPV,
+          umma_bf16_ta(tt + kPaOCol, tt + kPaSCol + k * 8, vd + ((k * 2 * L::kGroup) >> 4), kIdPV,
                        n > 0 || k > 0);
         if (dual) {
           // V_j goes back before the wait for K_j+2: the other tile's chunk
