@@ -999,23 +999,16 @@ __device__ __forceinline__ float pa_max32(const uint32_t (&u)[32], float4 f) {
   return m;
 }
 
-// 32 columns of an output row as bf16, from the row's own thread: two stores
-// of a whole 32-byte sector each, or 16-byte stores where out is only
-// 16-byte aligned.
-__device__ __forceinline__ void pa_store_row(__nv_bfloat16* dst, const uint32_t (&x)[16],
-                                             bool wide) {
+// 16 columns of an output row as bf16: a whole 32-byte sector, or two 16-byte
+// stores where out is only 16-byte aligned.
+__device__ __forceinline__ void pa_store16(__nv_bfloat16* dst, const uint32_t (&x)[8], bool wide) {
   if (wide) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst + 16 * i),
-                   "r"(x[8 * i]), "r"(x[8 * i + 1]), "r"(x[8 * i + 2]), "r"(x[8 * i + 3]),
-                   "r"(x[8 * i + 4]), "r"(x[8 * i + 5]), "r"(x[8 * i + 6]), "r"(x[8 * i + 7])
-                   : "memory");
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(x[0]),
+                 "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+                 : "memory");
   } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      reinterpret_cast<uint4*>(dst)[i] =
-          make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+    reinterpret_cast<uint4*>(dst)[0] = make_uint4(x[0], x[1], x[2], x[3]);
+    reinterpret_cast<uint4*>(dst)[1] = make_uint4(x[4], x[5], x[6], x[7]);
   }
 }
 
@@ -1243,6 +1236,13 @@ __device__ __forceinline__ void pa_softmax(const PrefillParams& p, PaBars* bars,
           p.out + (static_cast<int64_t>(it->row + tk) * p.num_q_heads + it->h * p.group +
                    (r - rt * p.group)) * D;
       if (!whole && has) p.ws_ml[slot * kPaItemRows + row] = make_float2(m, l);
+      // The rows of a lane pair are stored by both its lanes, 32 bytes each:
+      // half as many lines per instruction as a row per lane.
+      const bool odd = lane & 1;
+      const uint64_t mine = has ? reinterpret_cast<uint64_t>(to) : 0;
+      const uint64_t theirs = __shfl_xor_sync(0xffffffffu, mine, 1);
+      __nv_bfloat16* pair[2] = {reinterpret_cast<__nv_bfloat16*>(odd ? theirs : mine),
+                                reinterpret_cast<__nv_bfloat16*>(odd ? mine : theirs)};
       if (whole) {
         const float inv = l == 0.f ? 0.f : 1.f / l;
         w0 *= inv;
@@ -1272,17 +1272,27 @@ __device__ __forceinline__ void pa_softmax(const PrefillParams& p, PaBars* bars,
 #pragma unroll
           for (int i = 0; i < 32; ++i) x[i] = 0.f;
         }
-        if (!has) continue;
         if (!whole) {
+          if (has) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            po[(8 * c + i) * kPaItemRows] =
-                make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+            for (int i = 0; i < 8; ++i)
+              po[(8 * c + i) * kPaItemRows] =
+                  make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+          }
         } else {
-          uint32_t y[16];
+          // even lanes take the first half of both rows' 32 columns
+          uint32_t y[2][8];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) y[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
-          pa_store_row(to + 32 * c, y, wide);
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t lo = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+            const uint32_t hi = pack_bf16x2(x[16 + 2 * i], x[16 + 2 * i + 1]);
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? lo : hi, 1);
+            y[0][i] = odd ? got : lo;
+            y[1][i] = odd ? hi : got;
+          }
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            if (pair[k] != nullptr) pa_store16(pair[k] + 32 * c + (odd ? 16 : 0), y[k], wide);
         }
       }
       if (!whole && (it->flags & kPaHead) && threadIdx.x == 32 * kPaSoftWarp)
