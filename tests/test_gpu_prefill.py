@@ -132,9 +132,10 @@ def test_partition_does_not_depend_on_blocks_and_repeats_bit_for_bit():
     assert pa.pa_get_device_error() == 0
 
 
+@pytest.mark.parametrize("fp8", FP8)
 @pytest.mark.parametrize("scale", [-0.3, 0.0, 1e-42, 4.0])
-def test_scales(scale):
-    c = Prompt([70, 2], [70, 333], 4, 2, 64, 16, seed=5)
+def test_scales(scale, fp8):
+    c = Prompt([70, 2], [70, 333], 4, 2, 64, 16, seed=5, fp8=fp8)
     _check(c, True, f"scale {scale}", scale=scale)
 
 
@@ -154,6 +155,39 @@ def test_large_scores_stay_finite_and_the_maximum_moves():
         # scale sum|q k| ~ 150, so a weight is off by up to 2 * 150 * 128 * 2^-24
         # = 2.3e-3, less than 2^-8: allow that much of the spread on top
         assert_rows(out, ref, spread * 1.8, "growing keys")
+    assert pa.pa_get_device_error() == 0
+
+
+@pytest.mark.parametrize("fp8", FP8)
+@pytest.mark.parametrize("d", [64, 128])
+def test_the_first_scores_are_far_below_the_maximum(d, fp8):
+    # the running maximum starts from a chunk's first 32 scores: here those
+    # are 2^40 and more below the rest in weight, in every chunk and piece
+    c = Prompt([40, 3], [700, 900], 4, 2, d, 16, seed=23)
+    for b, n in enumerate(c.lens):
+        t = np.arange(n)
+        low = torch.from_numpy(t % 128 < 32)
+        k = torch.ones(n, c.hkv, d)
+        k[low] = -1
+        k += torch.randn(n, c.hkv, d, generator=torch.Generator().manual_seed(b)) * 0.05
+        c.k[torch.from_numpy(c.tab[b][t // 16]).long(), :, torch.from_numpy(t % 16)] = k.to(torch.bfloat16)
+    c.q = (torch.ones_like(c.q.float()) + c.q.float() * 0.05).to(torch.bfloat16)
+    scale = 40.0 / d
+    if fp8:
+        kn, vn = c.k.nan_to_num().float().numpy(), c.v.nan_to_num().float().numpy()
+        ids, full = list(range(c.nb)), [16] * c.nb
+        from oracle import quantize as OQ
+        kq, ks = OQ.quantize_blocks(kn, ids, full)
+        vq, vs = OQ.quantize_blocks(vn, ids, full)
+        c.k, c.v, c.ks, c.vs = (torch.from_numpy(x) for x in (kq, vq, ks, vs))
+    for causal in (True, False):
+        for splits in (0, 1, 5):
+            out = _run(c, causal, splits, scale=scale)
+            torch.cuda.synchronize()
+            ref, spread = c.oracle(causal, scale)
+            # scores of magnitude 40 lose at most D 2^-24 sum|q k| scale = 128 *
+            # 2^-24 * 44 = 3.4e-4: less than the 2^-10 allowed
+            assert_rows(out, ref, spread, f"low first scores, splits {splits}")
     assert pa.pa_get_device_error() == 0
 
 
@@ -184,6 +218,22 @@ def test_one_token_a_sequence(hq, hkv, fp8):
         torch.cuda.synchronize()
         assert_rows(out, ref, spread, "offsets")
     assert pa.pa_get_device_error() == 0
+
+
+@pytest.mark.parametrize("fp8", FP8)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("lens", [[1500], [3, 2100], [0], [1, 1024, 700]])
+def test_one_token_of_few_sequences_over_a_long_table(lens, d, fp8):
+    # one or two sequences over tables of 1024 tokens and more take another
+    # split than batches do
+    c = Prompt([1] * len(lens), lens, 8, 2, d, 16, seed=22, fp8=fp8)
+    c.tab = np.pad(c.tab, ((0, 0), (0, 70)), constant_values=-1)
+    out = _run(c, False, single=True)
+    torch.cuda.synchronize()
+    assert pa.pa_get_device_error() == 0
+    ref, spread = c.oracle(False)
+    # as above: FP8 decode at head_dim 128 has one more rounding per weight
+    assert_rows(out, ref, spread * (2 if fp8 else 1), "no offsets")
 
 
 def test_single_token_over_one_state_is_its_value():
