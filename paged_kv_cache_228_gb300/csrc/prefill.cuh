@@ -966,13 +966,6 @@ __device__ __forceinline__ void pa_mma(const PrefillParams& p, PaBars* bars, int
 }
 
 // -------------------------------------------------------------- softmax ---
-// 32 of a thread's raw scores (columns c0 ...); columns from `valid` on
-// become -inf.
-__device__ __forceinline__ void pa_mask(uint32_t (&u)[32], int32_t c0, int32_t valid) {
-#pragma unroll
-  for (int i = 0; i < 32; ++i) u[i] = c0 + i < valid ? u[i] : 0xff800000u;
-}
-
 // The largest of 32 scores: three-input maxima in two chains.
 __device__ __forceinline__ float pa_max32(const uint32_t (&u)[32]) {
   float m[2] = {-INFINITY, -INFINITY};
@@ -1067,16 +1060,25 @@ __device__ __forceinline__ void pa_softmax(const PrefillParams& p, PaBars* bars,
       }
       tc_fence_after_sync();
       if (warp_has) {
+        // Columns that some row of the warp does not see become -inf in place,
+        // in a loop of its own: unrolled into the registers below it would be
+        // four times the code for the few chunks that need it.
+        const int32_t valid = lim - j * kPaChunk;
+#pragma unroll 1
+        for (int c = 3; c >= 0 && __any_sync(0xffffffffu, valid < 32 * c + 32); --c) {
+          uint32_t x[32];
+          tmem_ld32(tb + kPaSCol + 32 * c, x);
+          tmem_wait_ld();
+          const int32_t here = valid - 32 * c;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) x[i] = i < here ? x[i] : 0xff800000u;
+          tmem_st32(tb + kPaSCol + 32 * c, x);
+          tmem_wait_st();
+        }
         uint32_t u[4][32];
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld32(tb + kPaSCol + 32 * c, u[c]);
         tmem_wait_ld();
-        const int32_t valid = lim - j * kPaChunk;
-        if (__any_sync(0xffffffffu, valid < kPaChunk)) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            if (__any_sync(0xffffffffu, valid < 32 * c + 32)) pa_mask(u[c], 32 * c, valid);
-        }
         // FP8: the chunk's scales, one of each kind per 8 columns
         const float4* sk =
             reinterpret_cast<const float4*>(scales + (chunk % L::kScales) * kPaScaleFloats);
