@@ -1158,7 +1158,7 @@ __device__ __forceinline__ void pa_softmax(const PrefillParams& p, PaBars* bars,
             tmem_st16(tb + kPaSCol + 16 * c, pk);
           }
           const float sum = (sa.x + sa.y) + (sb.x + sb.y);
-          if (move || !__any_sync(0xffffffffu, sum > 65536.f || (m == -INFINITY && sum > 0.f)))
+          if (move || !__any_sync(0xffffffffu, sum > 65536.f || m == -INFINITY))
             break;
           move = true;
         }

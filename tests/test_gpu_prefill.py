@@ -191,6 +191,31 @@ def test_the_first_scores_are_far_below_the_maximum(d, fp8):
     assert pa.pa_get_device_error() == 0
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_keys_with_scores_of_minus_infinity_have_no_weight(d):
+    # the first 32 scores of every row are -inf, the others about -120, whose
+    # exponentials against any maximum but their own underflow
+    c = Prompt([40, 3], [700, 200], 4, 2, d, 16, seed=29)
+    c.q = c.q * 0.05
+    c.q[..., 0] = 1
+    c.k = c.k * 0.5
+    for b, n in enumerate(c.lens):
+        t = np.arange(n)
+        at = torch.from_numpy(c.tab[b][t // 16]).long(), torch.from_numpy(t % 16)
+        first = torch.full((n, c.hkv), -120.0 * d ** 0.5)
+        first[:32] = float("-inf")
+        c.k[at[0], :, at[1], 0] = first.to(torch.bfloat16)
+    for causal in (True, False):
+        for splits in (0, 1, 5):
+            out = _run(c, causal, splits)
+            torch.cuda.synchronize()
+            ref, spread = c.oracle(causal)
+            # scores are off by at most D 2^-24 sum|q k| scale < 128 * 2^-24 *
+            # 121 = 9.3e-4: less than the 2^-10 allowed
+            assert_rows(out, ref, spread, f"scores of -inf, splits {splits}")
+    assert pa.pa_get_device_error() == 0
+
+
 def test_empty_encoder_gives_zeros_and_padded_rows_stay():
     c = Prompt([3, 5, 0], [0, 17, 9], 8, 2, 128, 16, seed=7, pad_rows=9)
     out = _check(c, False, "empty encoder")
