@@ -77,9 +77,9 @@ template <bool FP8>
 struct PaRegs {
   static constexpr int kThreads = kPaThreads + (FP8 ? 128 : 0);
   static constexpr int kLaunch = FP8 ? 128 : 168;
-  static constexpr int kFew = FP8 ? 64 : 88;
-  static constexpr int kSoft = FP8 ? 184 : 208;
-  static constexpr int kConv = 80;
+  static constexpr int kFew = FP8 ? 56 : 88;
+  static constexpr int kSoft = FP8 ? 192 : 208;
+  static constexpr int kConv = 72;
   static_assert(128 * kFew + 256 * kSoft + (FP8 ? 128 * kConv : 0) <= kThreads * kLaunch,
                 "register split");
 };
@@ -93,7 +93,7 @@ constexpr int kPaItems = 4;            // item records in flight
 
 constexpr int kPaBarBytes = 1024;
 constexpr int kPaMaxCodeStages = 8;
-// per chunk and 8 tokens: k, log2 v, 1 / v
+// per chunk and 8 tokens: k sl, log2 v, 1 / v
 constexpr int kPaScaleFloats = 48;
 
 
@@ -580,7 +580,7 @@ __device__ __forceinline__ void pa_copies(const PrefillParams& p, PaBars* bars,
           const int src = (lane & 15) * 8 / box;
           const float x = __shfl_sync(0xffffffffu, f.x, src), y = __shfl_sync(0xffffffffu, f.y, src);
           float* to = scales + c * kPaScaleFloats;
-          to[lane] = lane < 16 ? x : log2f(y);
+          to[lane] = lane < 16 ? x * p.sl : log2f(y);
           if (lane < 16) to[32 + lane] = 1.f / y;
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_addr(&bars->scale_full[c]));
@@ -1083,16 +1083,16 @@ __device__ __forceinline__ void pa_softmax(const PrefillParams& p, PaBars* bars,
         const float4* sk =
             reinterpret_cast<const float4*>(scales + (chunk % L::kScales) * kPaScaleFloats);
         auto largest = [&](int c) {  // scaled scores of columns 32 c ..
-          return FP8 ? pa_max32(u[c], sk[c]) : pa_max32(u[c]);
+          return FP8 ? pa_max32(u[c], sk[c]) : pa_max32(u[c]) * sl;
         };
-        if (j == begin) m = largest(0) * sl;
+        if (j == begin) m = largest(0);
         bool move = false;  // m moves to the maximum of this chunk too
         float2 sa, sb;
 #pragma unroll 1
         while (true) {
           if (move) {
             const float mn =
-                fmaxf(m, fmaxf(fmaxf(largest(0), largest(1)), fmaxf(largest(2), largest(3))) * sl);
+                fmaxf(m, fmaxf(fmaxf(largest(0), largest(1)), fmaxf(largest(2), largest(3))));
             if (j > begin) {
               // O and l scale by alpha.  O holds the products through the
               // chunk before, all complete (these scores were issued after
@@ -1137,7 +1137,7 @@ __device__ __forceinline__ void pa_softmax(const PrefillParams& p, PaBars* bars,
                           gi[4] = {fi.x, fi.y, fi.z, fi.w};
 #pragma unroll
               for (int q = 0; q < 4; ++q) {
-                const float2 a2 = make_float2(sl * gk[q], sl * gk[q]);
+                const float2 a2 = make_float2(gk[q], gk[q]);
                 const float2 b2 = make_float2(neg + gl[q], neg + gl[q]);
                 float2 part;  // of the weights times v
 #pragma unroll
