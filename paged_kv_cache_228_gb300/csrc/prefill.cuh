@@ -651,15 +651,19 @@ __device__ __forceinline__ void pa_widen(PaBars* bars, uint32_t codes, uint32_t 
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       const uint32_t src = codes + cs * L::kCodes, dst = ring + st * L::kKV;
-      // all of the thread's codes into registers, and the copies may refill
-      // the stage while they are widened
+      // All of the thread's codes into registers, and the copies may refill
+      // the stage while they are widened.  The loads are volatile and fenced
+      // against the copies' writes: with plain ones and no fence, rows of V
+      // behind an item's start, where this warp waits long for the ring, held
+      // the next chunk's codes (in half of the calls made back to back).
       uint32_t w[kPer][4];
 #pragma unroll
       for (int i = 0; i < kPer; ++i)
-        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+        asm volatile("ld.volatile.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
                      : "=r"(w[i][0]), "=r"(w[i][1]), "=r"(w[i][2]), "=r"(w[i][3])
                      : "r"(src + (t + 128 * i) * 16)
                      : "memory");
+      fence_proxy_async_smem();  // reads before the copies' writes
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_addr(&bars->code_empty[cs]));
       if (use > 0) ok = pa_wait(smem_addr(&bars->empty[st]), (use - 1) & 1);

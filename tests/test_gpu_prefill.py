@@ -216,6 +216,70 @@ def test_keys_with_scores_of_minus_infinity_have_no_weight(d):
     assert pa.pa_get_device_error() == 0
 
 
+def test_fp8_chunks_are_read_before_the_copies_refill_their_stage():
+    # K = 0: every visible token weighs the same; V of chunk j is 1 in column j
+    # and 0 elsewhere: column j of a row counts its visible tokens of chunk j.
+    # Calls back to back, each with an output of its own.
+    d, bs, hkv, hq = 128, 16, 8, 64
+    news, lens = [1021, 1021], [9237, 9982]
+    need = [-(-n // bs) for n in lens]
+    nb = sum(need)
+    ids = torch.randperm(nb, generator=torch.Generator().manual_seed(31)).int()
+    tab = torch.full((2, max(need)), -1, dtype=torch.int32)
+    tab[0, :need[0]], tab[1, :need[1]] = ids[:need[0]], ids[need[0]:]
+    k = torch.zeros(nb, hkv, bs, d, dtype=torch.uint8, device="cuda")
+    v = torch.zeros(nb, hkv, bs, d, dtype=torch.uint8)
+    want = torch.zeros(sum(news), d, dtype=torch.float64)
+    for b, n in enumerate(lens):
+        t = torch.arange(n)
+        v[tab[b][t // bs].long(), :, t % bs, t // 128] = 0x38  # 1.0
+        lim = torch.arange(n - news[b], n) + 1
+        seen = (lim[:, None] - 128 * torch.arange(d)[None, :]).clamp(0, 128)
+        want[sum(news[:b]):sum(news[:b + 1])] = seen / lim[:, None]
+    one = torch.ones(nb, hkv, device="cuda")
+    q = torch.randn(sum(news), hq, d, device="cuda").to(torch.bfloat16)
+    start = torch.tensor([0, news[0], sum(news)], dtype=torch.int32, device="cuda")
+    kv, tab, v = torch.tensor(lens, dtype=torch.int32, device="cuda"), tab.cuda(), v.cuda()
+    ws = torch.empty(pa.pa_attention_workspace_size(2, hq, hkv, d), dtype=torch.uint8,
+                     device="cuda")
+    # weights and their sum are exact or nearly so (2^-10); one rounding to
+    # bf16, 2^-8.  One token of another chunk is 1 / 128 of the value: more.
+    want = want.cuda()[:, None, :]
+    outs = [torch.full_like(q, float("nan")) for _ in range(20)]
+    torch.cuda.synchronize()
+    for out in outs:
+        pa.pa_prefill(q, k, v, tab, start, kv, d ** -0.5, out, ws, k_scale=one, v_scale=one)
+    for i, out in enumerate(outs):
+        err = (out.double() - want).abs() - (2.0 ** -8 + 2.0 ** -10) * want
+        assert bool((err <= 0).all()), f"call {i}: {int((err > 0).sum())} values off"
+    assert pa.pa_get_device_error() == 0
+
+
+@pytest.mark.parametrize("fp8", FP8)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+def test_calls_back_to_back_give_the_same_bits(causal, d, fp8):
+    # two batches in turn over one workspace, nothing between the launches
+    cases = (Prompt([130, 1, 300, 7], [900, 400, 300, 4100], 16, 4, d, 16, seed=37, fp8=fp8),
+             Prompt([5] * 9, [700 + 90 * i for i in range(9)], 16, 4, d, 32, seed=38, fp8=fp8))
+    devs = [c.device() for c in cases]
+    ws = torch.full((max(_ws(c).numel() for c in cases),), 255, dtype=torch.uint8, device="cuda")
+    fn = pa.pa_prefill if causal else pa.pa_cross_attention
+    outs = [torch.full(devs[i % 2]["q"].shape, float("nan"), dtype=torch.bfloat16, device="cuda")
+            for i in range(24)]
+    torch.cuda.synchronize()
+    for i, out in enumerate(outs):
+        c, x = cases[i % 2], devs[i % 2]
+        fn(x["q"], x["k"], x["v"], x["tab"], x["start"], x["lens"], c.scale, out, ws,
+           k_scale=x["ks"], v_scale=x["vs"])
+    torch.cuda.synchronize()
+    assert pa.pa_get_device_error() == 0
+    for i, out in enumerate(outs):
+        if i < 2:
+            assert_rows(out, *cases[i].oracle(causal), what=f"batch {i}")
+        assert torch.equal(out, outs[i % 2]), f"call {i}"
+
+
 def test_empty_encoder_gives_zeros_and_padded_rows_stay():
     c = Prompt([3, 5, 0], [0, 17, 9], 8, 2, 128, 16, seed=7, pad_rows=9)
     out = _check(c, False, "empty encoder")
