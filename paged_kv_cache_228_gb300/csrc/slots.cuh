@@ -22,6 +22,12 @@
 // cluster barrier and rank 0 writes them after it.  Neither kernel lets its
 // dependents start early (a decode kernel reads seq_lens before it waits for
 // its predecessor), and each thread's writes are performed before it exits.
+//
+// Measured inside a captured graph: 256 sequences that grow by one token
+// 4.3 us, a map of 58 thousand slots 4.6 us (11.3 with one token a thread in a
+// cluster), 256 finished sequences 5.9 us, 1500 that give back up to 8 tokens
+// 6.9 us.  A launch with nothing to do is some 2 us of each; the bytes (0.5
+// MB at most) are nothing.
 #pragma once
 
 #include <cooperative_groups.h>
