@@ -1177,7 +1177,9 @@ __device__ __forceinline__ void pa_softmax(const PrefillParams& p, PaBars* bars,
             tmem_st16(tb + kPaSCol + 16 * c, pk);
           }
           const float sum = (sa.x + sa.y) + (sb.x + sb.y);
-          if (move || !__any_sync(0xffffffffu, sum > 65536.f || m == -INFINITY))
+          // Rows without a token have no say: behind the last token of a
+          // group that does not divide 128 the tile holds earlier contents.
+          if (move || !__any_sync(0xffffffffu, has && (sum > 65536.f || m == -INFINITY)))
             break;
           move = true;
         }
