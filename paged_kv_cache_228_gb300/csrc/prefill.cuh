@@ -157,10 +157,10 @@ struct PaBars {
   uint64_t q_raw;             // a query tile before its sign or zero is applied
   uint64_t q_free[kPaTiles];  // the item's last score product of the tile done
   uint64_t s_full[kPaTiles];  // S of the tile's chunk written (and its last product done)
-  uint64_t p_full[kPaTiles];  // P of the tile's chunk written
+  uint64_t p_full[kPaTiles];  // P of the tile's chunk written, and the tile's turn
   uint64_t o_last[kPaTiles];  // the tile's last product of the item done
   uint64_t ml_full, o_free;   // dual items: tile 1's (m, l) written; its O read
-  uint64_t turn[kPaTiles];    // the other tile's MMAs of its turn have been issued
+  uint64_t turn;              // tile 0's first MMAs of an item issued: tile 1's first turn
   uint64_t mma_done[kPaTiles];
   int32_t bad;
   uint32_t tmem;
@@ -850,6 +850,9 @@ __device__ __forceinline__ void pa_items(const PrefillParams& p, PaBars* bars,
 // both tiles' MMAs would end together, and both softmaxes and then both
 // products would run at the same time for good; one after the other they
 // stay half a period apart.
+// A turn is an arrival on the barrier that the softmax's P completes: a wait
+// of its own behind that one, though long since complete, cost each chunk
+// some 300 of its 3250 cycles.
 //
 // A stage is free once both threads have passed it; for chunks of the other
 // tile (dual items, causal tiles that end earlier) this one only arrives,
@@ -866,8 +869,7 @@ __device__ __forceinline__ void pa_mma(const PrefillParams& p, PaBars* bars, int
   const uint64_t qd = smem_desc_sw128(sq + t * L::kQ, 16, 1024);
   PaItems items;
   PaRing<L::kStages> r;
-  uint32_t qph = 0, pph = 0, tph = 0;  // parity of the next queries, P, turn
-  bool owed = false;  // a turn of the other tile's that this one has not waited for
+  uint32_t qph = 0, pph = 0, tph = 0;  // parity of the next queries, P, first turn
   bool ok = true;
   auto full = [&]() { return pa_wait(smem_addr(&bars->full[r.stage]), r.phase); };
   // the stage of a chunk that is not this tile's
@@ -888,8 +890,8 @@ __device__ __forceinline__ void pa_mma(const PrefillParams& p, PaBars* bars, int
       const int32_t end = t == 0 ? end0 : end1;
       const bool dual = (it->flags & kPaDual) != 0;
       const int32_t step = dual ? 2 : 1;
-      // turns of the item: chunks that both tiles have
-      const int32_t both = dual ? 0 : min(end0, end1) - j0;
+      // turns of the item: chunks that both tiles have, if tile 0 has two
+      const int32_t both = dual || end0 - j0 < 2 ? 0 : min(end0, end1) - j0;
       int32_t j = j0;
       if (dual && t == 1) {
         pass();
@@ -922,14 +924,15 @@ __device__ __forceinline__ void pa_mma(const PrefillParams& p, PaBars* bars, int
         const uint64_t vd = smem_desc_sw128(ring + vst * L::kKV, 1024, L::kGroup);
         r.advance();
         if (more && !dual) ok = ok && full();
+        // tile 0's turn n comes behind tile 1's n - 1, tile 1's behind tile 0's n;
+        // without one the thread arrives in the other's place
+        if (t == 1 && n == 0 && both > 0) {
+          ok = ok && pa_wait(smem_addr(&bars->turn), tph);
+          tph ^= 1u;
+        }
+        if (n == 0 || n >= both + (t == 0 ? 1 : 0)) mbar_arrive(smem_addr(&bars->p_full[t]));
         ok = ok && pa_wait(smem_addr(&bars->p_full[t]), pph);
         pph ^= 1u;
-        // tile 0's turn n comes behind tile 1's n - 1, tile 1's behind tile 0's n
-        if (ok && (owed || (t == 0 ? n >= 1 && n <= both : n < both))) {
-          ok = pa_wait(smem_addr(&bars->turn[t]), tph);
-          tph ^= 1u;
-          owed = false;
-        }
         if (!ok) break;
         tc_fence_after_sync();
 #pragma unroll
@@ -949,7 +952,13 @@ __device__ __forceinline__ void pa_mma(const PrefillParams& p, PaBars* bars, int
           }
         }
         if (more) scores();
-        if (n < both) mbar_arrive(smem_addr(&bars->turn[1 - t]));
+        if (n < both) {
+          if (t == 1) {
+            if (n + 1 < end0 - j0) mbar_arrive(smem_addr(&bars->p_full[0]));
+          } else {
+            mbar_arrive(smem_addr(n == 0 ? &bars->turn : &bars->p_full[1]));
+          }
+        }
         if (more) {
           umma_commit(smem_addr(&bars->s_full[t]));
           if (j + 2 * step >= end) umma_commit(smem_addr(&bars->q_free[t]));
@@ -961,8 +970,6 @@ __device__ __forceinline__ void pa_mma(const PrefillParams& p, PaBars* bars, int
           if (!dual) umma_commit(smem_addr(&bars->empty[vst]));
         }
       }
-      // tile 1's last turn, where tile 0 has no further chunk of its own
-      if (t == 0 && both > 0 && end - j0 <= both) owed = true;
       // chunks behind the tile's last one
       if (dual) j -= 1;
       for (; j < j1 && ok; ++j) {
@@ -1365,9 +1372,8 @@ __global__ void __launch_bounds__(PaRegs<FP8>::kThreads, 1)
       mbar_init(smem_addr(&bars->q_full[t]), 1);
       mbar_init(smem_addr(&bars->q_free[t]), 1);
       mbar_init(smem_addr(&bars->s_full[t]), 1);
-      mbar_init(smem_addr(&bars->p_full[t]), 4);
+      mbar_init(smem_addr(&bars->p_full[t]), 5);
       mbar_init(smem_addr(&bars->o_last[t]), 1);
-      mbar_init(smem_addr(&bars->turn[t]), 1);
       mbar_init(smem_addr(&bars->mma_done[t]), 1);
     }
     for (int i = 0; i < kPaItems; ++i) {
@@ -1375,6 +1381,7 @@ __global__ void __launch_bounds__(PaRegs<FP8>::kThreads, 1)
       mbar_init(smem_addr(&bars->item_empty[i]), 1 + kPaTiles * 5 + (FP8 ? 4 : 0));
     }
     mbar_init(smem_addr(&bars->q_raw), 1);
+    mbar_init(smem_addr(&bars->turn), 1);
     mbar_init(smem_addr(&bars->ml_full), 4);
     mbar_init(smem_addr(&bars->o_free), 4);
     bars->bad = 0;
