@@ -32,14 +32,14 @@
 //     v 2^(s k sl - m) = 2^(s (k sl) + (log2 v - m)).
 //
 // What bounds it, measured (32 query and 8 KV heads, head_dim 128, bf16,
-// captured graph).  One prompt of 8192 tokens: 390 us, 1.41 PFLOP/s, tensor
-// pipe 61 % busy, DRAM 6 %: per chunk and tile the chain scores -> registers
-// -> exponentials -> weights back -> two products, of which two tiles hide
-// half.  8 prompts of 64 to 2048 tokens: 49 us, of which chunks 24, item ends
-// (the last product, rows out, the next item's first scores) 9, set-up, plan
-// and merge 12.  48 sequences of 4 to 8 drafted tokens over 0.5 to 4 thousand:
-// 63 us for 329 MB, DRAM 67 %.  FP8, 64 / 8 heads, 2 x 1021 tokens over 8 to 9
-// thousand: 611 us, 1.0 PFLOP/s; without any widening it would be 541.
+// captured graph).  One prompt of 8192 tokens: 377 us, 1.46 PFLOP/s, DRAM 6 %:
+// per chunk and tile the chain scores -> registers -> exponentials -> weights
+// back -> two products, of which two tiles hide half.  8 prompts of 64 to 2048
+// tokens: 49 us, of which chunks 23, item ends (the last product, rows out, the
+// next item's first scores) 9, set-up, plan and merge 12.  48 sequences of 4
+// to 8 drafted tokens over 0.5 to 4 thousand: 62.5 us for 329 MB, DRAM 67 %.
+// FP8, 64 / 8 heads, 2 x 1021 tokens over 8 to 9 thousand: 590 us, 1.03
+// PFLOP/s, of which the widening costs some 12 %.
 // Rows per tile: M = 128 is what one CTA's product takes at full rate, and two
 // tiles with scores and output fill the 512 tensor-memory columns at D = 128.
 #pragma once
@@ -640,8 +640,8 @@ __device__ __forceinline__ void e4m3x4_to_bf16x2x2(uint32_t w, uint32_t& lo, uin
 // two slabs share their banks, so threads of the second slab write their two
 // chunks in the other order.  Bound by issue slots and shared memory that the
 // softmax and the products use too: a chunk of 2 x 1021 tokens over 8 to 9
-// thousand takes 541 us without these warps' work, 616 with it (553 with V's
-// alone).
+// thousand that took 616 us took 541 without these warps' work and 553 with
+// V's alone.
 template <int D>
 __device__ __forceinline__ void pa_widen(PaBars* bars, uint32_t codes, uint32_t ring) {
   using L = PaSmem<D, true>;
