@@ -1470,11 +1470,14 @@ pa_status attention_entry(bool causal, const void* q, const void* k_cache, const
       items * num_kv_heads * (chunks + kPaItemCost) > 0xffffffffll - (1 << 20))
     return PA_ERR_UNSUPPORTED;
   // One token a sequence: the decode kernels, whose rows fit the batch, but
-  // for one or two sequences over long tables the wider split of the kernel
-  // here (one of 2000 tokens, 32 / 8 heads: bf16 d 128 12.7 against 21.1 us,
-  // FP8 d 64 14.8 against 22.5; four 14.2 against 15.8; 200 tokens 9.6 against
-  // 7.9).  FP8 at d 128 decodes on tcgen05 (9.8 against 16.8).
-  const bool few = num_seqs <= 2 && max_blocks_per_seq >= 1024 / block_size &&
+  // for a few sequences over long tables the wider split of the kernel here
+  // (32 / 8 heads, 2000 tokens, in us against the decode kernels: bf16 d 128 one
+  // sequence 12.5 / 21.0, four 14.2 / 15.8, eight 17.1 / 16.8; d 64 11.4 / 20.5,
+  // 12.0 / 15.8, 15.0 / 14.7; 500 tokens about the same; FP8 d 64 one 14.8 /
+  // 22.9, four 17.3 / 20.1 but 31 / 26 over 8000).  FP8 at d 128 decodes on
+  // tcgen05 (17.5 / 9.9).
+  const bool few = num_seqs <= (kv_dtype == PA_KV_BF16 ? 4 : 2) &&
+                   max_blocks_per_seq >= 1024 / block_size &&
                    !(kv_dtype == PA_KV_FP8_E4M3 && head_dim == 128);
   if (q_start == nullptr && group <= kMaxG && !few)
     return decode_entry(q, k_cache, v_cache, k_scale, v_scale, kv_dtype, block_tables,
