@@ -314,10 +314,11 @@ def test_one_token_a_sequence(hq, hkv, fp8):
 
 @pytest.mark.parametrize("fp8", FP8)
 @pytest.mark.parametrize("d", [64, 128])
-@pytest.mark.parametrize("lens", [[1500], [3, 2100], [0], [1, 1024, 700]])
+@pytest.mark.parametrize("lens", [[1500], [3, 2100], [0], [1, 1024, 700], [2000, 0, 129, 1],
+                                  [1100, 5, 600, 64, 1]])
 def test_one_token_of_few_sequences_over_a_long_table(lens, d, fp8):
-    # one or two sequences over tables of 1024 tokens and more take another
-    # split than batches do
+    # up to four sequences (two for FP8) over tables of 1024 tokens and more
+    # take another split than batches do
     c = Prompt([1] * len(lens), lens, 8, 2, d, 16, seed=22, fp8=fp8)
     c.tab = np.pad(c.tab, ((0, 0), (0, 70)), constant_values=-1)
     out = _run(c, False, single=True)
