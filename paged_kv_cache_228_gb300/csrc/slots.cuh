@@ -26,8 +26,8 @@
 // Measured inside a captured graph: 256 sequences that grow by one token
 // 4.3 us, a map of 58 thousand slots 4.6 us (11.3 with one token a thread in a
 // cluster), 256 finished sequences 5.8 us, 1500 that give back up to 8 tokens
-// 6.5 us (7.0 before a tile's lengths were loaded ahead).  A launch with nothing to do is some 2 us of each; the bytes (0.5
-// MB at most) are nothing.
+// 6.5 us (7.0 before a tile's lengths were loaded ahead).  A launch with
+// nothing to do is some 2 us of each; the bytes (0.5 MB at most) are nothing.
 #pragma once
 
 #include <cooperative_groups.h>
